@@ -64,6 +64,9 @@ typedef struct lora_pool_s *lora_pool; /* opaque; owned by the library */
 typedef struct lora_plan_s *lora_plan; /* opaque routing plan; owned by the library */
 typedef struct lora_loader_s *lora_loader; /* opaque host-to-slot loader; owned by the library */
 typedef struct lora_residency_s *lora_residency; /* opaque slot residency manager */
+typedef struct lora_kv_s *lora_kv;     /* opaque quantised key/value cache of one layer */
+typedef struct lora_attend_plan_s *lora_attend_plan; /* opaque attention plan of one step's batch */
+typedef struct lora_verifier_s *lora_verifier; /* opaque workspace of lora_verify */
 
 typedef enum { LORA_F32 = 0, LORA_F16 = 1, LORA_BF16 = 2 } lora_dtype;
 
@@ -83,6 +86,14 @@ typedef enum { LORA_MODE_AUTO = 0, LORA_MODE_FUSED = 1, LORA_MODE_SEPARATE = 2 }
 /* Limits of this build. */
 #define LORA_MAX_SLOTS 1024  /* n_slots per pool */
 #define LORA_MAX_RANK 64     /* max_rank per pool */
+
+#define LORA_KV_MAX_HEADS 256          /* key/value heads of a cache */
+#define LORA_KV_MAX_PAGE 1024          /* tokens of a page (a power of two, at least 16) */
+#define LORA_ATTEND_MAX_TOKENS 65536   /* sequences, groups and new tokens of a plan */
+#define LORA_ATTEND_MAX_PAGES (1 << 26) /* pages a plan's sequences and prefixes hold together */
+#define LORA_VERIFY_MAX_SEQS 65535     /* sequences of a verifier */
+#define LORA_VERIFY_MAX_VOCAB (1 << 24)
+#define LORA_VERIFY_MAX_DRAFTS 63      /* drafted tokens of one sequence */
 
 /* Status codes. */
 #define LORA_OK 0
@@ -406,6 +417,147 @@ typedef struct {
 } lora_residency_stats;
 
 int lora_residency_stats_read(lora_residency r, lora_residency_stats *out);
+
+/* ------------------------------------------- the step around the linears -- */
+
+/* What a serving step runs between the query/key/value projections and the
+ * output projection, and after the head: the quantised cache, attention over
+ * it, and the verification of drafted tokens.  Tokens of one tenant share an
+ * adapter, so their keys and values of a common prefix are the same and are
+ * held and computed once ["LLM 多 LoRA 推理服务工程 2026", KV reuse section].
+ * All calls are asynchronous on `stream` unless they say otherwise, neither
+ * allocate nor wait, and may be captured into a HIP graph. */
+
+/* A paged cache of one layer's keys and values in 8 bits, on the current HIP
+ * device.  Token slot s is token s % page_size of page s / page_size.  A row
+ * (one token of one head, head_dim values x) is held as e4m3 elements and one
+ * power of two:
+ *     s = the least whole number >= -64 with max|x| <= 448 * 2^s
+ *     e = x * 2^-s rounded to e4m3 (nearest, ties to even), stands for e * 2^s
+ * A row whose key or value holds a value that is not finite is poisoned: its
+ * key and value read back as NaN throughout, and the outputs of every query
+ * row that sees it are NaN; no other row's are.  Rows never written are 0.
+ *   n_pages >= 1, page_size a power of two of 16 .. LORA_KV_MAX_PAGE,
+ *   n_pages * page_size < 2^31; n_kv_heads 1 .. LORA_KV_MAX_HEADS;
+ *   head_dim 64 or 128; dtype LORA_F16 or LORA_BF16: of the keys and values
+ *   written and read, and of lora_attend's queries and outputs.
+ * Bytes: n_pages * page_size * n_kv_heads * 2 * (head_dim + 1).
+ * Errors: LORA_EINVAL, LORA_ENOMEM, LORA_EHIP. */
+int lora_kv_create(int n_pages, int page_size, int n_kv_heads, int head_dim, lora_dtype dtype, lora_kv *out);
+
+/* Waits for the device, then frees the cache.  kv == NULL is a no-op. */
+int lora_kv_destroy(lora_kv kv);
+
+/* Quantise keys and values of n_tokens tokens into their slots.
+ *   k, v      device, [n_tokens][n_kv_heads][head_dim], tokens k_stride /
+ *             v_stride elements apart (multiples of 8, at least n_kv_heads *
+ *             head_dim): parts of a fused projection's output need no copy
+ *   slots     device int32 [n_tokens]: the token's slot, or -1: not written.
+ *             Any other value outside the cache is not written and counted
+ *             (lora_kv_poll_errors).  No slot twice in one call.
+ * Errors (nothing enqueued): LORA_EINVAL, LORA_EHIP. */
+int lora_kv_write(lora_kv kv, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                  const int32_t *slots, int n_tokens, void *stream);
+
+/* Read slots back: k, v device [n_tokens][n_kv_heads][head_dim], contiguous,
+ * the values held, rounded once to the cache's dtype.  A slot outside the
+ * cache (-1 among them) reads as NaN and is counted.  Slots may repeat.
+ * Errors (nothing enqueued): LORA_EINVAL, LORA_EHIP. */
+int lora_kv_read(lora_kv kv, const int32_t *slots, int n_tokens, void *k, void *v, void *stream);
+
+/* Read and clear the count of slots that writes and reads found outside the
+ * cache.  Waits for the device.  Errors: LORA_EINVAL, LORA_EHIP. */
+int lora_kv_poll_errors(lora_kv kv, uint64_t *n_invalid_slots);
+
+/* One step's batch, host memory (read before lora_attend_plan_set returns).
+ * Sequence s has q_len[s] new tokens, the next q_len[s] rows of q and out,
+ * and kv_len[s] tokens of its own in the cache, the new ones among them; page
+ * list entries page0[s] .. page0[s + 1] - 1 hold them in order.  It belongs
+ * to group[s], whose prefix_len tokens come before its own, or to none (-1).
+ * New token j sees the whole prefix and its sequence's own tokens up to
+ * itself: the first kv_len[s] - q_len[s] + j + 1.  A token that sees nothing
+ * has output 0 and lse -inf. */
+typedef struct {
+    int32_t n_seqs, n_groups;
+    const int32_t *q_len, *kv_len, *group;  /* [n_seqs] */
+    const int32_t *pages, *page0;           /* page0 [n_seqs + 1] */
+    const int32_t *prefix_len;              /* [n_groups] */
+    const int32_t *prefix_pages, *prefix_page0; /* prefix_page0 [n_groups + 1] */
+} lora_attend_batch;
+
+/* A plan: how one batch's attention is cut into work for the device, made
+ * once a step and used by every layer's lora_attend (the routing plan's
+ * counterpart).  It holds the batch's lists and the workspace of partial
+ * results.  Allocates once, here.
+ *   n_heads a multiple of n_kv_heads, at most 32 times it.
+ * Errors: LORA_EINVAL (sizes out of range), LORA_ENOMEM, LORA_EHIP. */
+int lora_attend_plan_create(int max_seqs, int max_groups, int max_tokens, int max_pages, int n_heads,
+                            int n_kv_heads, int head_dim, lora_attend_plan *out);
+
+/* Waits for the device, then frees the plan.  plan == NULL is a no-op. */
+int lora_attend_plan_destroy(lora_attend_plan plan);
+
+/* Plan a batch on caches of kv's geometry: the host cuts it, and the plan goes
+ * to the device on `stream` (not while that is being captured: LORA_EINVAL).
+ * Every list is checked first: lengths below 0, groups and page ids out of
+ * range, fewer pages than a length needs are LORA_EINVAL, more new tokens
+ * than max_tokens LORA_ETOKENS, a cache of other heads or head_dim
+ * LORA_EMISMATCH; the plan is then empty until the next one.
+ * Plan and attention share the plan's memory: calls on one plan on different
+ * streams are ordered by the caller.  A captured lora_attend reads the plan as
+ * it is when the graph runs, so a graph may be replayed after a new plan. */
+int lora_attend_plan_set(lora_attend_plan plan, lora_kv kv, const lora_attend_batch *batch, void *stream);
+
+/* out = softmax(scale * q k^T) v for the planned batch, the values as the cache
+ * holds them, each group's prefix read once for all of its query rows.
+ *   kv     a cache of the planned geometry (pages, page size, heads,
+ *          head_dim), else LORA_EMISMATCH
+ *   q      device, [tokens][n_heads][head_dim], tokens q_stride elements
+ *          apart (a multiple of 8); query head h reads key/value head
+ *          h / (n_heads / n_kv_heads)
+ *   out    device, [tokens][n_heads][head_dim], contiguous; not q
+ *   lse    device float [tokens][n_heads], log(sum(exp(scale * q k^T))), or NULL
+ * Scores, maxima, sums and outputs are held in fp32; the weights are rounded
+ * to fp16 (11 bits) for the product with the values, the output once.
+ * Errors (nothing enqueued): LORA_EINVAL (no plan set, pointers, strides, scale
+ * not finite), LORA_EMISMATCH, LORA_EHIP. */
+int lora_attend(lora_kv kv, lora_attend_plan plan, const void *q, int64_t q_stride, float scale, void *out,
+                float *lse, void *stream);
+
+/* The workspace of lora_verify, for up to max_seqs sequences a call.
+ * Errors: LORA_EINVAL, LORA_ENOMEM, LORA_EHIP. */
+int lora_verifier_create(int max_seqs, lora_verifier *out);
+
+/* Waits for the device, then frees it.  v == NULL is a no-op. */
+int lora_verifier_destroy(lora_verifier v);
+
+/* Keep or replace drafted tokens.  Sequence s has rows row0[s] .. row0[s + 1] -
+ * 1 of p_target, one for each of its n drafted tokens and one for the token
+ * after them (n = 0: that one alone); draft and p_draft hold the drafted
+ * tokens alone, sequence s's from row0[s] - s.
+ *   p_target   device [n_rows][vocab], p_draft device [n_rows - n_seqs][vocab],
+ *              probabilities in dtype (any lora_dtype)
+ *   draft      device int32 [n_rows - n_seqs]
+ *   row0       device int32 [n_seqs + 1], strictly ascending from 0 to n_rows
+ *   u          device float [n_rows], of [0, 1)
+ * Drafted token i is kept while u[i] * p_draft[i][d] < p_target[i][d], exactly.
+ * One token is drawn after the k kept ones, with u[k]: from max(0, p_target -
+ * p_draft) of row k if a draft was refused there, from p_target's row n if
+ * none was (and where nothing of the difference is above 0): the first index
+ * at which the running sum, in fp64, passes u[k] times the whole.
+ *   accepted   device int32 [n_seqs]: k
+ *   tokens     device int32 [n_rows]: at row0[s], the k kept tokens, the drawn
+ *              one, then -1
+ * accepted is -1, and the sequence's tokens are -1, where a drafted token lies
+ * outside the vocabulary or the row to draw from has no weight (no entry above
+ * 0, or a sum that is not finite); also, with no token written, where the
+ * sequence's two entries of row0 do not ascend, leave no row for each sequence
+ * before and after it, or hold over LORA_VERIFY_MAX_DRAFTS drafts.
+ * Errors (nothing enqueued): LORA_EINVAL, LORA_ETOKENS (n_seqs), LORA_EHIP.
+ * Calls on one verifier on different streams are ordered by the caller. */
+int lora_verify(lora_verifier v, const void *p_target, const void *p_draft, lora_dtype dtype, int vocab,
+                const int32_t *draft, const int32_t *row0, const float *u, int n_seqs, int n_rows,
+                int32_t *tokens, int32_t *accepted, void *stream);
 
 /* ---------------------------------------------------------- observation -- */
 

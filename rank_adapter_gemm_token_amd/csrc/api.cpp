@@ -18,6 +18,7 @@
 #include <vector>
 
 #include "../../include/lora.h"
+#include "host.hpp"
 #include "internal.hpp"
 #include "ledger.hpp"
 #include "residency.hpp"
@@ -26,39 +27,19 @@ namespace {
 
 thread_local std::string g_last_hip;
 
-int hip_fail(hipError_t e) {
+}  // namespace
+
+int lora::hip_fail(hipError_t e) {
     g_last_hip = hipGetErrorString(e);
     return LORA_EHIP;
 }
 
-#define HIP_TRY(expr)                               \
-    do {                                            \
-        hipError_t e_ = (expr);                     \
-        if (e_ != hipSuccess) return hip_fail(e_);  \
-    } while (0)
+namespace {
 
-// Make the pool's device current for the duration of a call.
-class DeviceGuard {
-public:
-    explicit DeviceGuard(int dev) {
-        if (hipGetDevice(&prev_) != hipSuccess) {
-            prev_ = -1;
-            return;
-        }
-        if (prev_ != dev) err_ = hipSetDevice(dev);
-    }
-    ~DeviceGuard() {
-        int cur = -1;
-        if (prev_ >= 0 && hipGetDevice(&cur) == hipSuccess && cur != prev_) (void)hipSetDevice(prev_);
-    }
-    hipError_t error() const { return err_; }
-
-private:
-    int prev_ = -1;
-    hipError_t err_ = hipSuccess;
-};
-
-size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+using lora::align_up;
+using lora::aligned;
+using lora::DeviceGuard;
+using lora::hip_fail;
 
 // Default fused/separate threshold of gfx950.  The threshold is tuned per GPU
 // model ("LLM 多 LoRA 推理服务工程 2026", SRE list item 11; the routing-layer
@@ -241,8 +222,6 @@ hipError_t drain_inflight(lora_pool p) {
     if (p->noalloc_used) return hipEventSynchronize(p->noalloc_done);
     return hipSuccess;
 }
-
-bool aligned(const void *ptr, size_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; }
 
 // Publish slot entry `ent` so that every apply sees either the old entry in
 // all of its kernels or the new one in all of them (the decode path reads the

@@ -1,0 +1,413 @@
+// attend.hip -- attention of a batch's new tokens over the quantised cache,
+// with the prefix that a group of sequences shares computed once for all of
+// its query rows.
+//
+// In the log2 domain, for one query row over keys t with scores s_t, value
+// exponents b_t (v_t = 2^b_t v8_t) and c = scale * log2(e):
+//     x_t = c s_t + b_t,   m = max x_t,   p_t = 2^(x_t - m)
+//     O = sum p_t v8_t,    l = sum p_t 2^-b_t,   out = O / l,
+//     lse = ln 2 * (m + log2 l).
+// The value's exponent goes into the weight, so that the values' elements
+// feed the matrix instruction as they are; p_t stays near or below 1 for
+// values of any size and is exact enough in 16 bits.
+//
+// Both products are computed transposed, S^T = K Q^T and O^T = V^T P^T: the
+// keys' rows of S^T come out in the lanes that P^T needs them in, so the
+// weights never leave the registers.  A wave takes 64 keys at a time straight
+// from the cache into registers, 16 bytes a lane; no key is read by two waves
+// of an item.  Each wave keeps m, l and O of its own keys, and the workgroup
+// joins its four at the end.
+#include "attend_plan.hpp"
+#include "dtype.hpp"
+#include "kv_internal.hpp"
+
+namespace lora {
+
+namespace {
+
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+
+constexpr float LN2 = 0.69314718055994530942f;
+// The running maximum is moved only when a score passes it by this much
+// (log2): p stays below 2^8, far inside fp16, and most tiles scale nothing.
+constexpr float SLACK = 8.0f;
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Eight e4m3 elements (two words) as an MFMA operand, scaled by a power of two.
+template <int DT>
+__device__ __forceinline__ typename Elem<DT>::vec8 widen(uint32_t lo, uint32_t hi, float scale) {
+    if constexpr (DT == DT_F16) {
+        const f16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, scale, false);
+        const f16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, scale, true);
+        const f16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, scale, false);
+        const f16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, scale, true);
+        return f16x8_t{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+    } else {
+        const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+        const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+        const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+        const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+        return bf16x8_t{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+    }
+}
+
+__device__ __forceinline__ int byte_of(const u32x4_t &w, int i) { return (w[i / 4] >> (8 * (i % 4))) & 255; }
+
+__device__ __forceinline__ float pow2(int byte) { return __uint_as_float(static_cast<uint32_t>(byte) << 23); }
+
+constexpr int lds_floats(int D, int QB) { return ATTEND_WAVES * 16 * QB * (D + 4 + 2); }
+
+// One item for one key/value head, by one workgroup.  QB blocks of 16 query
+// rows; row = token of the item x query head of the key head.
+template <int DT, int D, int QB>
+__device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendItem &it, const AttendToken *toks,
+                                            const int32_t *page_list, int kvh, float *lds) {
+    using V8 = typename Elem<DT>::vec8;
+    constexpr int NC = D / 64;   // 64-element parts of a key's row: 16 bytes a lane each
+    constexpr int NH = D / 16;   // 16-element rows of V^T
+    constexpr int ROWS = 16 * QB;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int r = lane & 15, g = lane >> 4;
+    const int32_t *pages = page_list + it.page0;
+
+    // Queries: lane (r, g) holds row r of each block, elements 64 c + 16 g + 8 h .. + 7.
+    V8 qf[QB][2 * NC];
+    int lim[QB];  // keys the row sees
+#pragma unroll
+    for (int b = 0; b < QB; ++b) {
+        const int row = b * 16 + r, i = row / a.gq;
+        const int at = i < it.n_tok ? i : 0;
+        const int head = kvh * a.gq + row - i * a.gq;
+        const uint16_t *q = a.q + toks[at].token * a.q_stride + static_cast<long>(head) * D;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) qf[b][2 * c + h] = load8<V8>(q + c * 64 + g * 16 + h * 8);
+        const int l = it.limit0 + at * it.step;
+        lim[b] = l < it.end ? l : it.end;
+    }
+    // Below this every row sees every key.
+    const int all = it.limit0 < it.end ? it.limit0 : it.end;
+
+    float m[QB], l[QB];
+    f32x4_t o[NH][QB];
+#pragma unroll
+    for (int b = 0; b < QB; ++b) {
+        m[b] = -INFINITY;
+        l[b] = 0.0f;
+#pragma unroll
+        for (int h = 0; h < NH; ++h) o[h][b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    // Of a tile of 64 keys, block j of 16 is keys 16 j .. 16 j + 15.  S^T is
+    // computed in four products x = 0..3 whose row 4 j + i is key 16 j + 4 x
+    // + i; lane (r, g) then holds the scores of keys 16 g .. 16 g + 15, in
+    // order, of query row r.  Keys: lane (r, g) loads bytes 64 c + 16 g of
+    // key 16 (r / 4) + 4 x + r % 4.  Values: lane (r, g) loads element 16 h +
+    // r of block g's 16 keys.
+    const int t_end = (it.end + ATTEND_TILE - 1) / ATTEND_TILE;
+    int t = it.begin / ATTEND_TILE + wave;
+    const int last_block = it.end > 0 ? (it.end - 1) / KV_BLOCK : 0;
+    const int page_mask = (1 << a.page_shift) - 1;
+
+    // First row of the 16 rows of block `blk` (blocks past the end: the last one).
+    auto block_row = [&](int blk) {
+        blk = blk < last_block ? blk : last_block;
+        const int key = blk * KV_BLOCK;
+        const long page = pages[key >> a.page_shift];
+        return ((page * a.kv_heads + kvh) << a.page_shift) + (key & page_mask);
+    };
+    u32x4_t kw[4][NC], vw[NH], ke, ve;
+    auto load_k = [&](long R) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                kw[x][c] = *reinterpret_cast<const u32x4_t *>(a.k + (R + 4 * x + (r & 3)) * D + c * 64 + g * 16);
+        ke = *reinterpret_cast<const u32x4_t *>(a.kexp + R);
+    };
+    auto load_v = [&](long R) {
+#pragma unroll
+        for (int h = 0; h < NH; ++h) vw[h] = *reinterpret_cast<const u32x4_t *>(a.v + R * D + (h * 16 + r) * KV_BLOCK);
+        ve = *reinterpret_cast<const u32x4_t *>(a.vexp + R);
+    };
+    long kR = 0, vR = 0;
+    if (t < t_end) {
+        load_k(block_row(4 * t + (r >> 2)));
+        load_v(block_row(4 * t + g));
+        kR = block_row(4 * (t + ATTEND_WAVES) + (r >> 2));
+        vR = block_row(4 * (t + ATTEND_WAVES) + g);
+    }
+
+    for (; t < t_end; t += ATTEND_WAVES) {
+        const int key0 = t * ATTEND_TILE;
+        const bool more = t + ATTEND_WAVES < t_end;
+        // Scores.  bf16 holds any element times its scale; fp16 does for
+        // keys within 2^-15 of the tile's largest scale, and what is lost of
+        // the others is below 2^-24 of the largest, so the tile's scale is
+        // taken out of the conversion there.
+        float kscale[4], cs = a.scale;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int b = (ke[x] >> (8 * (r & 3))) & 255;
+            kscale[x] = pow2(b);
+            if constexpr (DT == DT_F16) kscale[x] = __uint_as_float(static_cast<uint32_t>(b));
+        }
+        if constexpr (DT == DT_F16) {
+            int top = 1;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int key = key0 + 16 * (r >> 2) + 4 * x + (r & 3);
+                const int b = static_cast<int>(__float_as_uint(kscale[x]));
+                top = key < it.end && b > top ? b : top;
+            }
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1) {
+                const int other = __shfl_xor(top, d, 64);
+                top = other > top ? other : top;
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int b = static_cast<int>(__float_as_uint(kscale[x])) - top + KV_EXP_BIAS;
+                kscale[x] = pow2(b < 1 ? 1 : b > 254 ? 254 : b);
+            }
+            cs *= pow2(top);
+        }
+        f32x4_t s[4][QB];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+#pragma unroll
+            for (int b = 0; b < QB; ++b) s[x][b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const V8 kf = widen<DT>(kw[x][c][2 * h], kw[x][c][2 * h + 1], kscale[x]);
+#pragma unroll
+                    for (int b = 0; b < QB; ++b) s[x][b] = Elem<DT>::mfma(kf, qf[b][2 * c + h], s[x][b]);
+                }
+        }
+        if (more) load_k(kR);
+
+        float be[16], ib[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int b = byte_of(ve, i);
+            be[i] = static_cast<float>(b) - static_cast<float>(KV_EXP_BIAS);
+            // (A poisoned row's is 0: its score is NaN where it is seen, and its weight 0 where not.)
+            ib[i] = pow2(b < 2 * KV_EXP_BIAS ? 2 * KV_EXP_BIAS - b : 0);
+        }
+#pragma unroll
+        for (int b = 0; b < QB; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i / 4][b][i % 4] = fmaf(s[i / 4][b][i % 4], cs, be[i]);
+        if (key0 + ATTEND_TILE > all) {
+#pragma unroll
+            for (int b = 0; b < QB; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (key0 + 16 * g + i >= lim[b]) s[i / 4][b][i % 4] = -INFINITY;
+        }
+        float top[QB];
+        bool moves = false;
+#pragma unroll
+        for (int b = 0; b < QB; ++b) {
+            float v = s[0][b][0];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) v = fmaxf(v, s[i / 4][b][i % 4]);
+            v = fmaxf(v, __shfl_xor(v, 16, 64));
+            v = fmaxf(v, __shfl_xor(v, 32, 64));
+            top[b] = v;
+            moves |= v > m[b] + SLACK;
+        }
+        if (__any(moves)) {
+#pragma unroll
+            for (int b = 0; b < QB; ++b) {
+                const float to = fmaxf(m[b], top[b]);
+                const float f = to == m[b] ? 1.0f : exp2_fast(m[b] - to);
+                m[b] = to;
+                l[b] *= f;
+#pragma unroll
+                for (int h = 0; h < NH; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[h][b][i] *= f;
+            }
+        }
+        // Weights, 8 keys an operand: half x holds keys 8 x .. 8 x + 7 of the lane's 16.
+        f16x8_t p[2][QB];
+#pragma unroll
+        for (int b = 0; b < QB; ++b) {
+            const float ref = m[b] == -INFINITY ? 0.0f : m[b];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float w = exp2_fast(s[i / 4][b][i % 4] - ref);
+                l[b] = fmaf(w, ib[i], l[b]);
+                p[i / 8][b][i % 8] = static_cast<_Float16>(w);
+            }
+        }
+        if (more) {
+            const int next = t + 2 * ATTEND_WAVES;
+            kR = block_row(4 * next + (r >> 2));
+        }
+#pragma unroll
+        for (int h = 0; h < NH; ++h)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const f16x8_t vf = widen<DT_F16>(vw[h][2 * x], vw[h][2 * x + 1], 1.0f);
+#pragma unroll
+                for (int b = 0; b < QB; ++b) o[h][b] = Elem<DT_F16>::mfma(vf, p[x][b], o[h][b]);
+            }
+        if (more) {
+            load_v(vR);
+            vR = block_row(4 * (t + 2 * ATTEND_WAVES) + g);
+        }
+    }
+
+    // Join the four waves: O scaled to the workgroup's maximum, added in LDS.
+    float *lo = lds, *lm = lds + ATTEND_WAVES * ROWS * (D + 4);
+#pragma unroll
+    for (int b = 0; b < QB; ++b) {
+        l[b] += __shfl_xor(l[b], 16, 64);
+        l[b] += __shfl_xor(l[b], 32, 64);
+        if (g == 0) {
+            lm[(wave * ROWS + b * 16 + r) * 2] = m[b];
+            lm[(wave * ROWS + b * 16 + r) * 2 + 1] = l[b];
+        }
+#pragma unroll
+        for (int h = 0; h < NH; ++h)
+            *reinterpret_cast<f32x4_t *>(lo + (wave * ROWS + b * 16 + r) * (D + 4) + h * 16 + g * 4) = o[h][b];
+    }
+    __syncthreads();
+    const int n_rows = it.n_tok * a.gq;
+    constexpr int PER = D / 4;  // lanes of a row, four elements each
+    for (int at = threadIdx.x; at < n_rows * PER; at += 256) {
+        const int row = at / PER, d = at % PER * 4;
+        float mw[ATTEND_WAVES], M = -INFINITY, L = 0.0f;
+#pragma unroll
+        for (int w = 0; w < ATTEND_WAVES; ++w) {
+            mw[w] = lm[(w * ROWS + row) * 2];
+            M = fmaxf(M, mw[w]);
+        }
+        const float ref = M == -INFINITY ? 0.0f : M;
+        f32x4_t sum{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int w = 0; w < ATTEND_WAVES; ++w) {
+            const float f = exp2_fast(mw[w] - ref);
+            L = fmaf(f, lm[(w * ROWS + row) * 2 + 1], L);
+            sum += f * *reinterpret_cast<const f32x4_t *>(lo + (w * ROWS + row) * (D + 4) + d);
+        }
+        const int i = row / a.gq, head = kvh * a.gq + row - i * a.gq;
+        if (it.part0 >= 0) {
+            const long at_part = static_cast<long>(it.part0 + i) * a.heads + head;
+            *reinterpret_cast<f32x4_t *>(a.part_o + at_part * D + d) = sum;
+            if (d == 0) {
+                a.part_ml[at_part * 2] = M;
+                a.part_ml[at_part * 2 + 1] = L;
+            }
+        } else {
+            const long at_out = static_cast<long>(toks[i].token) * a.heads + head;
+            // No key seen: zeros.  (L is NaN, not 0, where a seen key is poisoned.)
+            const float f = L == 0.0f ? 0.0f : 1.0f / L;
+            typename Elem<DT>::raw w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = Elem<DT>::from_f(sum[j] * f);
+            *reinterpret_cast<uint2 *>(a.out + at_out * D + d) = *reinterpret_cast<const uint2 *>(w);
+            if (d == 0 && a.lse != nullptr) a.lse[at_out] = LN2 * (M + log2f(L));
+        }
+    }
+    __syncthreads();  // the next item writes LDS again
+}
+
+// Whether the plan is for caches like this one: a graph that was captured with
+// one cache may be replayed after a plan for others, whose pages it must not
+// follow.
+__device__ __forceinline__ bool plan_fits(const AttendArgs &a, const AttendHeader *h) {
+    return h->page_size == 1 << a.page_shift && h->n_pages == a.n_pages;
+}
+
+template <int DT, int D>
+__global__ __launch_bounds__(256, 2) void k_attend(AttendArgs a) {
+    extern __shared__ float lds[];
+    const AttendHeader *h = reinterpret_cast<const AttendHeader *>(a.meta);
+    const AttendItem *items = reinterpret_cast<const AttendItem *>(a.meta + sizeof(AttendHeader));
+    const AttendToken *toks = reinterpret_cast<const AttendToken *>(a.meta + h->token_off);
+    const int32_t *pages = reinterpret_cast<const int32_t *>(a.meta + h->page_off);
+    const int n = plan_fits(a, h) ? h->n_items * a.kv_heads : 0;
+    // The grid has a workgroup for each item of the plan at launch; a graph
+    // replayed after a new plan may find more.
+    for (int w = blockIdx.x; w < n; w += gridDim.x) {
+        const int i = w / a.kv_heads, kvh = w - i * a.kv_heads;
+        const AttendItem it = items[i];
+        if (it.n_tok * a.gq <= 16)
+            attend_item<DT, D, 1>(a, it, toks + it.tok0, pages, kvh, lds);
+        else
+            attend_item<DT, D, 2>(a, it, toks + it.tok0, pages, kvh, lds);
+    }
+}
+
+// Join the partial results of each (token, head): D / 4 lanes a row.
+template <int DT, int D>
+__global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
+    const AttendHeader *h = reinterpret_cast<const AttendHeader *>(a.meta);
+    const AttendToken *toks = reinterpret_cast<const AttendToken *>(a.meta + h->token_off);
+    constexpr int PER = D / 4, ROWS = 256 / PER;
+    const long n = h->n_split > 0 && plan_fits(a, h) ? static_cast<long>(h->n_tokens) * a.heads : 0;
+    for (long row = static_cast<long>(blockIdx.x) * ROWS + threadIdx.x / PER; row < n;
+         row += static_cast<long>(gridDim.x) * ROWS) {
+        const int s = static_cast<int>(row / a.heads), head = static_cast<int>(row - static_cast<long>(s) * a.heads);
+        const AttendToken tk = toks[s];
+        const int parts = tk.n[0] + tk.n[1];
+        if (parts == 0) continue;
+        const int d = threadIdx.x % PER * 4;
+        float M = -INFINITY, L = 0.0f;
+        f32x4_t sum{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int k = 0; k < 2; ++k)
+            for (int j = 0; j < tk.n[k]; ++j) {
+                const long at = static_cast<long>(tk.part[k] + j * tk.stride[k]) * a.heads + head;
+                const float pm = a.part_ml[at * 2], pl = a.part_ml[at * 2 + 1];
+                const f32x4_t po = *reinterpret_cast<const f32x4_t *>(a.part_o + at * D + d);
+                const float to = fmaxf(M, pm);
+                const float ref = to == -INFINITY ? 0.0f : to;
+                const float f0 = exp2_fast(M - ref), f1 = exp2_fast(pm - ref);
+                M = to;
+                L = L * f0 + pl * f1;
+                sum = sum * f0 + po * f1;
+            }
+        const long at_out = static_cast<long>(tk.token) * a.heads + head;
+        const float f = L == 0.0f ? 0.0f : 1.0f / L;
+        typename Elem<DT>::raw w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = Elem<DT>::from_f(sum[j] * f);
+        *reinterpret_cast<uint2 *>(a.out + at_out * D + d) = *reinterpret_cast<const uint2 *>(w);
+        if (d == 0 && a.lse != nullptr) a.lse[at_out] = LN2 * (M + log2f(L));
+    }
+}
+
+template <int DT, int D>
+hipError_t run(const AttendArgs &a, int n_items, int n_tokens, hipStream_t st) {
+    constexpr size_t lds = lds_floats(D, ATTEND_ROWS / 16) * sizeof(float);
+    static const hipError_t set = hipFuncSetAttribute(reinterpret_cast<const void *>(k_attend<DT, D>),
+                                                      hipFuncAttributeMaxDynamicSharedMemorySize,
+                                                      static_cast<int>(lds));
+    if (set != hipSuccess) return set;
+    const long wgs = static_cast<long>(n_items) * a.kv_heads;
+    k_attend<DT, D><<<static_cast<unsigned>(wgs < 1 ? 1 : wgs > 65536 ? 65536 : wgs), 256, lds, st>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const long rows = static_cast<long>(n_tokens) * a.heads, per = 256 / (D / 4);
+    const long joins = (rows + per - 1) / per;
+    k_attend_join<DT, D><<<static_cast<unsigned>(joins < 1 ? 1 : joins > 65536 ? 65536 : joins), 256, 0, st>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attend(const AttendArgs &a, int dtype, int dim, int n_items, int n_tokens, hipStream_t st) {
+    if (dtype == DT_F16)
+        return dim == 128 ? run<DT_F16, 128>(a, n_items, n_tokens, st) : run<DT_F16, 64>(a, n_items, n_tokens, st);
+    return dim == 128 ? run<DT_BF16, 128>(a, n_items, n_tokens, st) : run<DT_BF16, 64>(a, n_items, n_tokens, st);
+}
+
+}  // namespace lora

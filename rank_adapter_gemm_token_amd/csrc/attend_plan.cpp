@@ -1,0 +1,230 @@
+// attend_plan.cpp -- cutting one batch's attention into work items
+// (attend_plan.hpp).
+#include "attend_plan.hpp"
+
+#include <algorithm>
+#include <cstring>
+
+#include "../../include/lora.h"
+
+namespace lora {
+
+namespace {
+
+int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// Cost of one tile of keys for an item of `rows` query rows, in tenths of the
+// time a tile takes with up to 16.
+int tile_cost(int rows) { return rows <= 16 ? 10 : 16; }
+
+}  // namespace
+
+AttendPlanner::AttendPlanner(int max_seqs, int max_groups, int max_tokens, int max_pages, int n_heads,
+                             int n_kv_heads)
+    : max_seqs_(max_seqs),
+      max_groups_(max_groups),
+      max_tokens_(max_tokens),
+      max_pages_(max_pages),
+      n_heads_(n_heads),
+      n_kv_heads_(n_kv_heads) {
+    const int gq = n_heads / n_kv_heads;
+    // A block has at least one token, of one sequence or of one group.
+    max_spans_ = 2 * max_tokens;
+    // plan() gives a span ceil(cost / target) items and the targets sum to
+    // ATTEND_SLOTS / n_kv_heads over all spans.
+    const int extra = ceil_div(ATTEND_SLOTS, n_kv_heads) + 1;
+    max_items_ = max_spans_ + extra;
+    // Every span's tokens once, and a block's tokens for each further item.
+    max_part_rows_ = 2 * max_tokens + extra * attend_block_tokens(gq);
+    items_.reserve(static_cast<size_t>(max_items_));
+    tokens_.reserve(static_cast<size_t>(max_tokens));
+    pages_.reserve(static_cast<size_t>(max_pages) + 1);
+    spans_.reserve(static_cast<size_t>(max_spans_));
+    seq_tok_.resize(static_cast<size_t>(max_seqs));
+    seq_page_.resize(static_cast<size_t>(max_seqs));
+    q_first_.resize(static_cast<size_t>(max_seqs));
+    grp_tok_.resize(static_cast<size_t>(max_groups) + 2);
+    grp_page_.resize(static_cast<size_t>(max_groups) + 1);
+}
+
+size_t AttendPlanner::max_bytes() const {
+    return sizeof(AttendHeader) + static_cast<size_t>(max_items_) * sizeof(AttendItem) +
+           static_cast<size_t>(max_tokens_) * sizeof(AttendToken) + (static_cast<size_t>(max_pages_) + 4) * 4;
+}
+
+void AttendPlanner::clear() {
+    items_.clear();
+    tokens_.clear();
+    pages_.clear();
+    spans_.clear();
+    part_rows_ = n_split_ = 0;
+}
+
+int AttendPlanner::check(const AttendBatch &b, const AttendGeometry &geo) const {
+    if (b.n_seqs < 0 || b.n_seqs > max_seqs_ || b.n_groups < 0 || b.n_groups > max_groups_) return LORA_EINVAL;
+    if (geo.n_heads != n_heads_ || geo.n_kv_heads != n_kv_heads_ || geo.page_size < 1 || geo.n_pages < 1)
+        return LORA_EINVAL;
+    if (b.n_seqs > 0 && (b.q_len == nullptr || b.kv_len == nullptr || b.group == nullptr || b.page0 == nullptr))
+        return LORA_EINVAL;
+    if (b.n_groups > 0 && (b.prefix_len == nullptr || b.prefix_page0 == nullptr)) return LORA_EINVAL;
+    int64_t tokens = 0, pages = 0;
+    // A row of pages: `len` keys in pages[first .. last).
+    auto row = [&](const int32_t *list, const int32_t *at, int i, int32_t len) {
+        if (len < 0 || len > ATTEND_MAX_KEYS || at[i] < 0 || at[i + 1] < at[i]) return false;
+        const int64_t need = (static_cast<int64_t>(len) + geo.page_size - 1) / geo.page_size;
+        if (need > at[i + 1] - at[i]) return false;
+        if (need > 0 && list == nullptr) return false;
+        for (int64_t k = 0; k < need; ++k)
+            if (list[at[i] + k] < 0 || list[at[i] + k] >= geo.n_pages) return false;
+        pages += need;
+        return true;
+    };
+    for (int s = 0; s < b.n_seqs; ++s) {
+        if (b.q_len[s] < 0 || b.group[s] < -1 || b.group[s] >= b.n_groups) return LORA_EINVAL;
+        if (!row(b.pages, b.page0, s, b.kv_len[s])) return LORA_EINVAL;
+        tokens += b.q_len[s];
+    }
+    for (int i = 0; i < b.n_groups; ++i)
+        if (!row(b.prefix_pages, b.prefix_page0, i, b.prefix_len[i])) return LORA_EINVAL;
+    if (tokens > max_tokens_) return LORA_ETOKENS;
+    if (pages > max_pages_) return LORA_EINVAL;
+    return LORA_OK;
+}
+
+int AttendPlanner::plan(const AttendBatch &b, const AttendGeometry &geo) {
+    clear();
+    const int rc = check(b, geo);
+    if (rc != LORA_OK) return rc;
+    page_size_ = geo.page_size;
+    n_pages_ = geo.n_pages;
+    const int gq = n_heads_ / n_kv_heads_;
+    const int block = attend_block_tokens(gq);
+
+    // Pages: each span's own, none that its length does not reach.
+    auto add_pages = [&](const int32_t *list, const int32_t *at, int i, int32_t len) {
+        const int first = static_cast<int>(pages_.size());
+        const int need = static_cast<int>((static_cast<int64_t>(len) + geo.page_size - 1) / geo.page_size);
+        if (need > 0) pages_.insert(pages_.end(), list + at[i], list + at[i] + need);
+        return first;
+    };
+    for (int i = 0; i < b.n_groups; ++i)
+        grp_page_[i] = add_pages(b.prefix_pages, b.prefix_page0, i, b.prefix_len[i]);
+    for (int s = 0; s < b.n_seqs; ++s) seq_page_[s] = add_pages(b.pages, b.page0, s, b.kv_len[s]);
+
+    // Query tokens sorted by group (group -1 last), sequences in order.
+    std::fill(grp_tok_.begin(), grp_tok_.end(), 0);
+    int total = 0;
+    for (int s = 0; s < b.n_seqs; ++s) {
+        q_first_[s] = total;
+        total += b.q_len[s];
+        grp_tok_[(b.group[s] < 0 ? b.n_groups : b.group[s]) + 1] += b.q_len[s];
+    }
+    for (int i = 0; i <= b.n_groups; ++i) grp_tok_[i + 1] += grp_tok_[i];
+    tokens_.resize(static_cast<size_t>(total));
+    {
+        // grp_tok_[i] walks through group i and ends at group i + 1's start.
+        for (int s = 0; s < b.n_seqs; ++s) {
+            int &at = grp_tok_[b.group[s] < 0 ? b.n_groups : b.group[s]];
+            seq_tok_[s] = at;
+            for (int j = 0; j < b.q_len[s]; ++j) {
+                AttendToken t{};
+                t.token = q_first_[s] + j;
+                tokens_[static_cast<size_t>(at + j)] = t;
+            }
+            at += b.q_len[s];
+        }
+    }
+
+    // Spans, and the tokens that none reaches (nothing to attend to).
+    int64_t cost = 0;
+    auto add_span = [&](int tok0, int n, int page0, int end, int limit0, int step, bool own) {
+        spans_.push_back(Span{tok0, n, page0, end, limit0, step, own, 1});
+        cost += static_cast<int64_t>(ceil_div(end, ATTEND_TILE)) * tile_cost(n * gq);
+    };
+    for (int i = 0; i < b.n_groups; ++i) {
+        const int first = i == 0 ? 0 : grp_tok_[i - 1], n = grp_tok_[i] - first;
+        if (b.prefix_len[i] == 0) continue;
+        for (int t = 0; t < n; t += block)
+            add_span(first + t, std::min(block, n - t), grp_page_[i], b.prefix_len[i], b.prefix_len[i], 0, false);
+    }
+    for (int s = 0; s < b.n_seqs; ++s) {
+        const int before = b.kv_len[s] - b.q_len[s];  // query token j sees before + j + 1 of its own
+        for (int t = 0; t < b.q_len[s]; t += block) {
+            const int n = std::min(block, b.q_len[s] - t);
+            const int end = before + t + n;
+            const bool prefix = b.group[s] >= 0 && b.prefix_len[b.group[s]] > 0;
+            // A block that sees nothing still has its rows to write.
+            if (end > 0 || !prefix)
+                add_span(seq_tok_[s] + t, n, seq_page_[s], std::max(0, end), before + t + 1, 1, true);
+        }
+    }
+
+    // Each item costs about an even share of the whole, four tiles at least
+    // (one for each wave).
+    const int64_t target =
+        std::max<int64_t>((cost * n_kv_heads_ + ATTEND_SLOTS - 1) / ATTEND_SLOTS, ATTEND_WAVES * tile_cost(1));
+    for (Span &s : spans_) {
+        const int tiles = ceil_div(s.end, ATTEND_TILE);
+        const int64_t c = static_cast<int64_t>(tiles) * tile_cost(s.n_tok * gq);
+        s.splits = static_cast<int>(
+            std::max<int64_t>(1, std::min<int64_t>((c + target - 1) / target, ceil_div(tiles, ATTEND_WAVES))));
+        for (int i = 0; i < s.n_tok; ++i) tokens_[static_cast<size_t>(s.tok0 + i)].n[s.own] = s.splits;
+    }
+    for (Span &s : spans_) {
+        // Alone: no token of the block has a result of another item.
+        bool alone = s.splits == 1;
+        for (int i = 0; alone && i < s.n_tok; ++i) alone = tokens_[static_cast<size_t>(s.tok0 + i)].n[!s.own] == 0;
+        const int tiles = ceil_div(s.end, ATTEND_TILE);
+        const int base = part_rows_;
+        for (int k = 0; k < s.splits; ++k) {
+            const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * k / s.splits);
+            const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (k + 1) / s.splits);
+            items_.push_back(AttendItem{s.tok0, s.n_tok, s.page0, t0 * ATTEND_TILE, std::min(s.end, t1 * ATTEND_TILE),
+                                        s.limit0, s.step, alone ? -1 : base + k * s.n_tok});
+        }
+        for (int i = 0; i < s.n_tok; ++i) {
+            AttendToken &t = tokens_[static_cast<size_t>(s.tok0 + i)];
+            if (alone) {
+                t.pad = 1;
+            } else {
+                t.part[s.own] = base + i;
+                t.stride[s.own] = s.n_tok;
+            }
+        }
+        if (!alone) part_rows_ += s.splits * s.n_tok;
+    }
+    for (AttendToken &t : tokens_) {
+        if (t.pad) t.n[0] = t.n[1] = 0;
+        t.pad = 0;
+        n_split_ += t.n[0] + t.n[1] > 0;
+    }
+    // The dearest first: what is left at the end is short.
+    std::sort(items_.begin(), items_.end(), [gq](const AttendItem &x, const AttendItem &y) {
+        const int64_t cx = static_cast<int64_t>(x.end - x.begin) * tile_cost(x.n_tok * gq);
+        const int64_t cy = static_cast<int64_t>(y.end - y.begin) * tile_cost(y.n_tok * gq);
+        if (cx != cy) return cx > cy;
+        if (x.tok0 != y.tok0) return x.tok0 < y.tok0;
+        return x.page0 != y.page0 ? x.page0 < y.page0 : x.begin < y.begin;
+    });
+    return LORA_OK;
+}
+
+size_t AttendPlanner::write(void *to) const {
+    AttendHeader h{};
+    h.n_items = static_cast<int32_t>(items_.size());
+    h.n_tokens = static_cast<int32_t>(tokens_.size());
+    h.n_split = n_split_;
+    h.page_size = page_size_;
+    h.n_pages = n_pages_;
+    const size_t items = items_.size() * sizeof(AttendItem), toks = tokens_.size() * sizeof(AttendToken);
+    h.token_off = static_cast<int32_t>(sizeof h + items);
+    h.page_off = static_cast<int32_t>(sizeof h + items + toks);
+    char *p = static_cast<char *>(to);
+    std::memcpy(p, &h, sizeof h);
+    if (items) std::memcpy(p + sizeof h, items_.data(), items);
+    if (toks) std::memcpy(p + h.token_off, tokens_.data(), toks);
+    if (!pages_.empty()) std::memcpy(p + h.page_off, pages_.data(), pages_.size() * 4);
+    return static_cast<size_t>(h.page_off) + pages_.size() * 4;
+}
+
+}  // namespace lora

@@ -1,0 +1,70 @@
+// kv_internal.hpp -- records and launchers shared by kv_api.cpp and the .hip
+// files of the cache, the attention over it and the draft verification.  Not
+// part of the public ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+namespace lora {
+
+// The quantised cache.  A row is one token of one key/value head: D elements
+// of e4m3, and an exponent byte b that scales them by 2^(b - 127).  Row
+// (page, head, offset) has the number R = (page * heads + head) * page_size +
+// offset.
+//   keys    element d of row R at byte R * D + d
+//   values  blocks of 16 rows are stored by element: element d of row R at
+//           byte (R - R % 16) * D + d * 16 + R % 16, so that the attention
+//           reads 16 keys' values of one element as one word
+//   kexp, vexp  the exponent bytes, one a row
+// Elements are finite, except that a row whose key or value has a value that
+// is not finite is POISONED: its key elements are NaN (its scores are then
+// NaN, wherever they are looked at, and nothing else is), its value elements
+// 0 and its vexp KV_POISON.
+constexpr int KV_BLOCK = 16;        // rows of a block of values
+constexpr int KV_POISON = 255;
+constexpr int KV_EXP_BIAS = 127;
+constexpr int KV_MIN_EXP = -64;     // least exponent kept: smaller values go to 0
+
+struct KvCache {
+    uint8_t *k, *v, *kexp, *vexp;
+    unsigned long long *err;
+    int n_pages, page_shift, heads, dim;  // page_size = 1 << page_shift
+    int dtype;
+};
+
+hipError_t launch_kv_write(const KvCache &c, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                           const int32_t *slots, int n_tokens, hipStream_t st);
+hipError_t launch_kv_read(const KvCache &c, const int32_t *slots, int n_tokens, void *k, void *v, hipStream_t st);
+
+struct AttendArgs {
+    const char *meta;      // AttendHeader, items, tokens, pages
+    const uint8_t *k, *v, *kexp, *vexp;
+    const uint16_t *q;
+    int64_t q_stride;      // elements from one token's heads to the next's
+    uint16_t *out;         // [tokens][heads][dim]
+    float *lse;            // [tokens][heads] or null
+    float *part_o;         // [part rows][heads][dim]
+    float *part_ml;        // [part rows][heads][2]
+    int heads, kv_heads, gq, page_shift, n_pages;
+    float scale;           // softmax scale times log2(e)
+};
+
+hipError_t launch_attend(const AttendArgs &a, int dtype, int dim, int n_items, int n_tokens, hipStream_t st);
+
+struct VerifyArgs {
+    const void *p, *q;
+    const int32_t *draft, *row0;
+    const float *u;
+    int32_t *tokens, *accepted;
+    double *sums;          // [seqs][VERIFY_CHUNKS][2]
+    unsigned *count;       // [seqs], 0 between calls
+    int n_seqs, n_rows, vocab, chunk, chunks;
+};
+constexpr int VERIFY_CHUNKS = 64;     // parts of a row at most
+constexpr int VERIFY_MAX_DRAFTS = 63; // drafted tokens of a sequence
+
+hipError_t launch_verify(const VerifyArgs &a, int dtype, hipStream_t st);
+
+}  // namespace lora

@@ -23,6 +23,13 @@ LORA_SEG_NONE, LORA_SEG_FUSED, LORA_SEG_SEPARATE = 0, 1, 2
 LORA_BASE_ONLY = -1
 LORA_MAX_SLOTS = 1024
 LORA_MAX_RANK = 64
+LORA_KV_MAX_HEADS = 256
+LORA_KV_MAX_PAGE = 1024
+LORA_ATTEND_MAX_TOKENS = 65536
+LORA_ATTEND_MAX_PAGES = 1 << 26
+LORA_VERIFY_MAX_SEQS = 65535
+LORA_VERIFY_MAX_VOCAB = 1 << 24
+LORA_VERIFY_MAX_DRAFTS = 63
 
 LORA_OK = 0
 LORA_EINVAL = -1
@@ -50,6 +57,9 @@ EXPORTS = ["lora_pool_create", "lora_pool_destroy", "lora_set_tenant_quota", "lo
            "lora_loader_create", "lora_loader_destroy", "lora_load_async", "lora_load_poll", "lora_load_wait",
            "lora_residency_create", "lora_residency_destroy", "lora_residency_set_share",
            "lora_residency_acquire", "lora_residency_release", "lora_residency_stats_read",
+           "lora_kv_create", "lora_kv_destroy", "lora_kv_write", "lora_kv_read", "lora_kv_poll_errors",
+           "lora_attend_plan_create", "lora_attend_plan_destroy", "lora_attend_plan_set", "lora_attend",
+           "lora_verifier_create", "lora_verifier_destroy", "lora_verify",
            "lora_pool_stats", "lora_tenant_bytes", "lora_poll_errors", "lora_profile_enable",
            "lora_profile_read", "lora_strerror", "lora_last_hip_error"]
 
@@ -76,6 +86,12 @@ class lora_profile(ctypes.Structure):
     _fields_ = [("calls", ctypes.c_int64), ("route_ms", ctypes.c_double), ("shrink_ms", ctypes.c_double),
                 ("gemm_ms", ctypes.c_double), ("expand_ms", ctypes.c_double),
                 ("kernel_ms", ctypes.c_double)]
+
+
+class lora_attend_batch(ctypes.Structure):
+    _fields_ = ([("n_seqs", ctypes.c_int32), ("n_groups", ctypes.c_int32)] +
+                [(n, ctypes.c_void_p) for n in ("q_len", "kv_len", "group", "pages", "page0", "prefix_len",
+                                                "prefix_pages", "prefix_page0")])
 
 
 _vp = ctypes.c_void_p
@@ -109,6 +125,19 @@ _lib.lora_residency_acquire.argtypes = [_vp, ctypes.c_uint64, ctypes.c_int32, _v
                                         ctypes.POINTER(_i), ctypes.POINTER(ctypes.c_uint64)]
 _lib.lora_residency_release.argtypes = [_vp, ctypes.c_uint64]
 _lib.lora_residency_stats_read.argtypes = [_vp, ctypes.POINTER(lora_residency_stats)]
+_i64 = ctypes.c_int64
+_lib.lora_kv_create.argtypes = [_i, _i, _i, _i, _i, ctypes.POINTER(_vp)]
+_lib.lora_kv_destroy.argtypes = [_vp]
+_lib.lora_kv_write.argtypes = [_vp, _vp, _i64, _vp, _i64, _vp, _i, _vp]
+_lib.lora_kv_read.argtypes = [_vp, _vp, _i, _vp, _vp, _vp]
+_lib.lora_kv_poll_errors.argtypes = [_vp, ctypes.POINTER(ctypes.c_uint64)]
+_lib.lora_attend_plan_create.argtypes = [_i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_vp)]
+_lib.lora_attend_plan_destroy.argtypes = [_vp]
+_lib.lora_attend_plan_set.argtypes = [_vp, _vp, ctypes.POINTER(lora_attend_batch), _vp]
+_lib.lora_attend.argtypes = [_vp, _vp, _vp, _i64, ctypes.c_float, _vp, _vp, _vp]
+_lib.lora_verifier_create.argtypes = [_i, ctypes.POINTER(_vp)]
+_lib.lora_verifier_destroy.argtypes = [_vp]
+_lib.lora_verify.argtypes = [_vp, _vp, _vp, _i, _i, _vp, _vp, _vp, _i, _i, _vp, _vp, _vp]
 _lib.lora_pool_stats.argtypes = [_vp, ctypes.POINTER(lora_stats)]
 _lib.lora_tenant_bytes.argtypes = [_vp, ctypes.c_int32, ctypes.POINTER(ctypes.c_uint64)]
 _lib.lora_poll_errors.argtypes = [_vp, ctypes.POINTER(ctypes.c_uint64)]
@@ -387,6 +416,146 @@ def lora_residency_stats_read(res):
     st = lora_residency_stats()
     _check(_lib.lora_residency_stats_read(res, ctypes.byref(st)), "lora_residency_stats_read")
     return {name: getattr(st, name) for name, _ in lora_residency_stats._fields_}
+
+
+# Caches (heads, head_dim, dtype) and attention plans (heads, head_dim, tokens
+# of the planned batch) created through this binding.
+_kvs = {}
+_attend_plans = {}
+
+
+def lora_kv_create(n_pages, page_size, n_kv_heads, head_dim, dtype):
+    """Returns the cache handle (an int).  dtype: torch dtype or LORA_F16/BF16."""
+    if isinstance(dtype, torch.dtype):
+        dtype = DTYPE_OF[dtype]
+    h = _vp()
+    _check(_lib.lora_kv_create(int(n_pages), int(page_size), int(n_kv_heads), int(head_dim), int(dtype),
+                               ctypes.byref(h)), "lora_kv_create")
+    _kvs[h.value] = (int(n_kv_heads), int(head_dim), TORCH_DTYPE[int(dtype)])
+    return h.value
+
+
+def lora_kv_destroy(kv):
+    _check(_lib.lora_kv_destroy(kv), "lora_kv_destroy")
+    _kvs.pop(kv, None)
+
+
+def _rows(t, n, heads, dim, dtype, what):
+    """Device pointer and token stride of an [n, heads, dim] tensor whose heads
+    are contiguous within a token."""
+    if t.dtype != dtype or not t.is_cuda:
+        raise ValueError("%s: expected a device tensor of %s, got %s on %s" % (what, dtype, t.dtype, t.device))
+    if t.dim() != 3 or t.shape[0] < n or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError("%s: expected [%d, %d, %d], got %s" % (what, n, heads, dim, tuple(t.shape)))
+    st = t.stride()
+    if st[2] != 1 or (heads > 1 and st[1] != dim):
+        raise ValueError("%s: a token's heads must be contiguous, got strides %s" % (what, st))
+    # A single row's stride says nothing.
+    return t.data_ptr(), st[0] if t.shape[0] > 1 else max(st[0], heads * dim)
+
+
+def _flat(t, numel, dtype, what):
+    """Device pointer of a contiguous device tensor of at least numel elements."""
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.numel() < numel:
+        raise ValueError("%s: expected %d contiguous elements of %s on the device, got %s of %s on %s"
+                         % (what, numel, dtype, tuple(t.shape), t.dtype, t.device))
+    return t.data_ptr()
+
+
+def lora_kv_write(kv, k, v, slots, n_tokens, stream=None):
+    """k, v: [n_tokens, n_kv_heads, head_dim], strided over tokens; slots: device int32."""
+    heads, dim, dtype = _kvs[kv]
+    kp, ks = _rows(k, n_tokens, heads, dim, dtype, "k")
+    vp, vs = _rows(v, n_tokens, heads, dim, dtype, "v")
+    _check(_lib.lora_kv_write(kv, kp, ks, vp, vs, _flat(slots, n_tokens, torch.int32, "slots"), n_tokens,
+                              _stream(stream)), "lora_kv_write")
+
+
+def lora_kv_read(kv, slots, n_tokens, k, v, stream=None):
+    heads, dim, dtype = _kvs[kv]
+    n = n_tokens * heads * dim
+    _check(_lib.lora_kv_read(kv, _flat(slots, n_tokens, torch.int32, "slots"), n_tokens, _flat(k, n, dtype, "k"),
+                             _flat(v, n, dtype, "v"), _stream(stream)), "lora_kv_read")
+
+
+def lora_kv_poll_errors(kv):
+    v = ctypes.c_uint64()
+    _check(_lib.lora_kv_poll_errors(kv, ctypes.byref(v)), "lora_kv_poll_errors")
+    return v.value
+
+
+def lora_attend_plan_create(max_seqs, max_groups, max_tokens, max_pages, n_heads, n_kv_heads, head_dim):
+    """Returns the plan handle (an int)."""
+    h = _vp()
+    _check(_lib.lora_attend_plan_create(int(max_seqs), int(max_groups), int(max_tokens), int(max_pages),
+                                        int(n_heads), int(n_kv_heads), int(head_dim), ctypes.byref(h)),
+           "lora_attend_plan_create")
+    _attend_plans[h.value] = [int(n_heads), int(head_dim), 0]
+    return h.value
+
+
+def lora_attend_plan_destroy(plan):
+    _check(_lib.lora_attend_plan_destroy(plan), "lora_attend_plan_destroy")
+    _attend_plans.pop(plan, None)
+
+
+def lora_attend_plan_set(plan, kv, q_len, kv_len, group, pages, page0, prefix_len=None, prefix_pages=None,
+                         prefix_page0=None, stream=None):
+    """The batch's lists as host int32 tensors (lora_attend_batch in lora.h)."""
+    def host(t, n, what):
+        if t is None:
+            if n > 0:
+                raise ValueError("%s: expected %d elements, got none" % (what, n))
+            return None
+        if t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < n:
+            raise ValueError("%s: expected %d contiguous host int32 elements, got %s of %s on %s"
+                             % (what, n, tuple(t.shape), t.dtype, t.device))
+        return t.data_ptr()
+    n_seqs = q_len.numel()
+    n_groups = 0 if prefix_len is None else prefix_len.numel()
+    b = lora_attend_batch(n_seqs, n_groups, host(q_len, n_seqs, "q_len"), host(kv_len, n_seqs, "kv_len"),
+                          host(group, n_seqs, "group"),
+                          host(pages, int(page0[-1]) if n_seqs else 0, "pages"),
+                          host(page0, n_seqs + 1 if n_seqs else 0, "page0"), host(prefix_len, n_groups, "prefix_len"),
+                          host(prefix_pages, int(prefix_page0[-1]) if n_groups else 0, "prefix_pages"),
+                          host(prefix_page0, n_groups + 1 if n_groups else 0, "prefix_page0"))
+    _attend_plans[plan][2] = 0
+    _check(_lib.lora_attend_plan_set(plan, kv, ctypes.byref(b), _stream(stream)), "lora_attend_plan_set")
+    _attend_plans[plan][2] = int(q_len.sum())
+
+
+def lora_attend(kv, plan, q, scale, out, lse=None, stream=None):
+    """q, out: [tokens, n_heads, head_dim] of the planned batch, q strided over tokens."""
+    heads, dim, tokens = _attend_plans[plan]
+    dtype = _kvs[kv][2]
+    qp, qs = _rows(q, tokens, heads, dim, dtype, "q")
+    _check(_lib.lora_attend(kv, plan, qp, qs, scale, _flat(out, tokens * heads * dim, dtype, "out"),
+                            None if lse is None else _flat(lse, tokens * heads, torch.float32, "lse"),
+                            _stream(stream)), "lora_attend")
+
+
+def lora_verifier_create(max_seqs):
+    """Returns the verifier handle (an int)."""
+    h = _vp()
+    _check(_lib.lora_verifier_create(int(max_seqs), ctypes.byref(h)), "lora_verifier_create")
+    return h.value
+
+
+def lora_verifier_destroy(verifier):
+    _check(_lib.lora_verifier_destroy(verifier), "lora_verifier_destroy")
+
+
+def lora_verify(verifier, p_target, p_draft, draft, row0, u, n_seqs, n_rows, tokens, accepted, stream=None):
+    """p_target: [n_rows, vocab]; p_draft: [n_rows - n_seqs, vocab] of the same dtype."""
+    vocab, dtype = p_target.shape[-1], p_target.dtype
+    n_drafts = max(0, n_rows - n_seqs)
+    i32 = torch.int32
+    _check(_lib.lora_verify(verifier, _flat(p_target, n_rows * vocab, dtype, "p_target"),
+                            _flat(p_draft, n_drafts * vocab, dtype, "p_draft"), DTYPE_OF[dtype], vocab,
+                            _flat(draft, n_drafts, i32, "draft"), _flat(row0, n_seqs + 1, i32, "row0"),
+                            _flat(u, n_rows, torch.float32, "u"), n_seqs, n_rows,
+                            _flat(tokens, n_rows, i32, "tokens"), _flat(accepted, n_seqs, i32, "accepted"),
+                            _stream(stream)), "lora_verify")
 
 
 def lora_pool_stats(pool):

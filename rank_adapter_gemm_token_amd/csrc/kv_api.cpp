@@ -299,7 +299,7 @@ int lora_verifier_create(int max_seqs, lora_verifier *out) {
     lora_verifier v = new (std::nothrow) lora_verifier_s;
     if (v == nullptr) return LORA_ENOMEM;
     v->max_seqs = max_seqs;
-    const size_t sums = static_cast<size_t>(max_seqs) * lora::VERIFY_CHUNKS * 2 * sizeof(double);
+    const size_t sums = static_cast<size_t>(max_seqs) * lora::VERIFY_PARTS * sizeof(double);
     const size_t total = sums + static_cast<size_t>(max_seqs) * sizeof(unsigned);
     hipError_t e = hipGetDevice(&v->device);
     if (e == hipSuccess) e = hipMalloc(reinterpret_cast<void **>(&v->mem), total);
@@ -355,12 +355,14 @@ int lora_verify(lora_verifier v, const void *p_target, const void *p_draft, lora
     a.n_seqs = n_seqs;
     a.n_rows = n_rows;
     a.vocab = vocab;
-    // Parts of 2048 elements (one pass of a workgroup), of more where that
-    // makes over VERIFY_CHUNKS of them.
-    constexpr int part = 2048;
-    const int parts = (vocab + part - 1) / part;
-    a.chunk = part * ((parts + lora::VERIFY_CHUNKS - 1) / lora::VERIFY_CHUNKS);
-    a.chunks = (vocab + a.chunk - 1) / a.chunk;
+    // Parts of one step, of more where that makes over VERIFY_PARTS of them;
+    // as many parts a workgroup as leaves about eight workgroups a CU (2048):
+    // each has the same few dependent reads before its first part.
+    const int steps = (vocab + lora::VERIFY_STEP - 1) / lora::VERIFY_STEP;
+    a.part = lora::VERIFY_STEP * ((steps + lora::VERIFY_PARTS - 1) / lora::VERIFY_PARTS);
+    a.parts = (vocab + a.part - 1) / a.part;
+    const int wgs = 2048 / n_seqs;  // of a sequence
+    a.group = wgs < 1 ? a.parts : (a.parts + wgs - 1) / wgs;
     HIP_TRY(lora::launch_verify(a, static_cast<int>(dtype), static_cast<hipStream_t>(stream)));
     return LORA_OK;
 }

@@ -58,11 +58,13 @@ struct VerifyArgs {
     const int32_t *draft, *row0;
     const float *u;
     int32_t *tokens, *accepted;
-    double *sums;          // [seqs][VERIFY_CHUNKS][2]
+    double *sums;          // [seqs][VERIFY_PARTS]
     unsigned *count;       // [seqs], 0 between calls
-    int n_seqs, n_rows, vocab, chunk, chunks;
+    int n_seqs, n_rows, vocab;
+    int part, parts, group;  // elements of a part, parts of a row, parts of a workgroup
 };
-constexpr int VERIFY_CHUNKS = 64;     // parts of a row at most
+constexpr int VERIFY_PARTS = 64;      // parts of a row at most
+constexpr int VERIFY_STEP = 2048;     // elements a workgroup takes at a time
 constexpr int VERIFY_MAX_DRAFTS = 63; // drafted tokens of a sequence
 
 hipError_t launch_verify(const VerifyArgs &a, int dtype, hipStream_t st);

@@ -18,6 +18,7 @@ namespace {
 
 constexpr int THREADS = 256;
 constexpr int STEP = 8;  // elements a thread takes at a time
+constexpr int NONE = 0x7FFFFFFF;
 
 template <int DT>
 struct Wide {
@@ -70,16 +71,39 @@ __device__ __forceinline__ double block_scan(double v, double *s) {
     return v;
 }
 
-// Workgroup (c, b): chunk c of the row that sequence b's new token is drawn
-// from.  Each finds that row itself (a handful of reads), adds its chunk up,
-// and the last of a sequence's workgroups to finish picks the chunk, reads it
-// once more and picks the token.
+// The sum of eight neighbouring weights, index i .. i + 7, those below hi.
+template <int DT>
+__device__ __forceinline__ double weights(const typename Elem<DT>::raw *p, const typename Elem<DT>::raw *q, int i,
+                                          int hi) {
+    float x[STEP] = {}, y[STEP] = {};
+    if (i + STEP <= hi) {
+        load_p<DT>(p + i, x);
+        if (q != nullptr) load_p<DT>(q + i, y);
+    } else {
+#pragma unroll
+        for (int j = 0; j < STEP; ++j)
+            if (i + j < hi) {
+                x[j] = Elem<DT>::to_f(p[i + j]);
+                if (q != nullptr) y[j] = Elem<DT>::to_f(q[i + j]);
+            }
+    }
+    double v = 0.0;
+#pragma unroll
+    for (int j = 0; j < STEP; ++j) v += weight(x[j], y[j]);
+    return v;
+}
+
+// The row that a sequence's new token is drawn from is cut into up to
+// VERIFY_PARTS parts.  Workgroup (c, b) finds that row of sequence b itself (a
+// handful of reads), adds up `group` of its parts, and the last of a
+// sequence's workgroups to finish picks the part, reads it once more and picks
+// the token.
 template <int DT>
 __global__ __launch_bounds__(THREADS) void k_verify(VerifyArgs a) {
     using raw = typename Elem<DT>::raw;
     const raw *p = static_cast<const raw *>(a.p), *q = static_cast<const raw *>(a.q);
     const int b = blockIdx.y, c = blockIdx.x, t = threadIdx.x, V = a.vocab;
-    __shared__ double s[THREADS / 64];
+    __shared__ double s[VERIFY_PARTS][THREADS / 64];
     __shared__ int found;
     __shared__ unsigned arrived;
 
@@ -92,7 +116,7 @@ __global__ __launch_bounds__(THREADS) void k_verify(VerifyArgs a) {
         return;
     }
     // Lane i looks at drafted token i.
-    const int lane = t & 63;
+    const int lane = t & 63, wave = t >> 6;
     bool keep = false, bad = false;
     int d = -1;
     if (lane < n) {
@@ -105,11 +129,11 @@ __global__ __launch_bounds__(THREADS) void k_verify(VerifyArgs a) {
         }
     }
     const bool any_bad = __ballot(bad) != 0;
-    const int kept = __builtin_ctzll(~__ballot(keep));  // n <= 63: a bit is left
+    const int kept = uniform(__builtin_ctzll(~__ballot(keep)));  // n <= 63: a bit is left
     if (any_bad) {
         // A drafted token that is none: no answer for the sequence.
         if (c == 0) {
-            for (int i = t; i <= n; i += THREADS) a.tokens[r0 + i] = -1;
+            if (t <= n) a.tokens[r0 + t] = -1;
             if (t == 0) a.accepted[b] = -1;
         }
         return;
@@ -117,67 +141,65 @@ __global__ __launch_bounds__(THREADS) void k_verify(VerifyArgs a) {
     const raw *pr = p + static_cast<long>(r0 + kept) * V;
     const raw *qr = kept < n ? q + static_cast<long>(r0 - b + kept) * V : nullptr;
 
-    // The chunk's sums: of max(0, p - q) and of p.
-    const int lo = c * a.chunk, hi = lo + a.chunk < V ? lo + a.chunk : V;
-    double rest = 0.0, whole = 0.0;
-    for (int i = lo + t * STEP; i < hi; i += THREADS * STEP) {
-        float x[STEP], y[STEP] = {};
-        if (i + STEP <= hi) {
-            load_p<DT>(pr + i, x);
-            if (qr != nullptr) load_p<DT>(qr + i, y);
-        } else {
-#pragma unroll
-            for (int j = 0; j < STEP; ++j) {
-                x[j] = i + j < hi ? Elem<DT>::to_f(pr[i + j]) : 0.0f;
-                y[j] = i + j < hi && qr != nullptr ? Elem<DT>::to_f(qr[i + j]) : 0.0f;
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < STEP; ++j) {
-            rest += weight(x[j], y[j]);
-            whole += weight(x[j], 0.0f);
-        }
-    }
-    rest = block_sum(rest, s);
-    whole = block_sum(whole, s);
-    double *sums = a.sums + static_cast<long>(b) * VERIFY_CHUNKS * 2;
-    if (t == 0) {
-        __hip_atomic_store(sums + 2 * c, rest, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __hip_atomic_store(sums + 2 * c + 1, whole, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        arrived = __hip_atomic_fetch_add(a.count + b, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-        found = 0x7FFFFFFF;
+    const int p0 = c * a.group, p1 = p0 + a.group < a.parts ? p0 + a.group : a.parts;
+#pragma unroll 2
+    for (int part = p0; part < p1; ++part) {
+        const int lo = part * a.part, hi = lo + a.part < V ? lo + a.part : V;
+        double v = 0.0;
+        for (int i = lo + t * STEP; i < hi; i += THREADS * STEP) v += weights<DT>(pr, qr, i, hi);
+        v = wave_sum(v);
+        if (lane == 0) s[part - p0][wave] = v;
     }
     __syncthreads();
-    if (arrived != static_cast<unsigned>(a.chunks - 1)) return;
+    double *sums = a.sums + static_cast<long>(b) * VERIFY_PARTS;
+    if (wave == 0) {
+        if (lane < p1 - p0)
+            __hip_atomic_store(sums + p0 + lane, (s[lane][0] + s[lane][1]) + (s[lane][2] + s[lane][3]),
+                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        // The sums are at the agent's coherence point before the workgroup is
+        // counted (a release at agent scope would write the whole L2 back:
+        // 480 us instead of 40 for 256 sequences).
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        if (lane == 0) {
+            arrived = __hip_atomic_fetch_add(a.count + b, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            found = NONE;
+        }
+    }
+    __syncthreads();
+    if (arrived != gridDim.x - 1) return;
     if (t == 0) __hip_atomic_store(a.count + b, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 
-    // Lane i holds chunk i's sums (VERIFY_CHUNKS is a wave's width).
-    double sr = 0.0, sw = 0.0;
-    if (lane < a.chunks) {
-        sr = __hip_atomic_load(sums + 2 * lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        sw = __hip_atomic_load(sums + 2 * lane + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    if (!(wave_sum(sr) > 0.0)) {
-        sr = sw;
-        qr = nullptr;
-    }
-    double run = sr;
+    // Lane i holds part i's sum (VERIFY_PARTS is a wave's width).
+    double part_sum = 0.0;
+    if (lane < a.parts) part_sum = __hip_atomic_load(sums + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    double run = part_sum;
 #pragma unroll
     for (int k = 1; k < 64; k <<= 1) {
         const double o = __shfl_up(run, k, 64);
         if (lane >= k) run += o;
     }
-    const double total = __shfl(run, 63, 64);
-    const double aim = static_cast<double>(a.u[r0 + kept]) * total;
-    // The first chunk whose running sum passes, or the last with any weight.
-    const unsigned long long passes = __ballot(run > aim), some = __ballot(sr > 0.0);
-    const bool drawn = total > 0.0 && total <= 1.7976931348623157e308 && some != 0;
+    double total = __shfl(run, 63, 64);
+    // The part to look in, and the running sum before it.
+    int from = 0, to = V;
+    double base = 0.0;
+    if (!(total > 0.0) && qr != nullptr) {
+        // Nothing of the difference is left: the target's row, as a whole.
+        qr = nullptr;
+        double v = 0.0;
+        for (int i = t * STEP; i < V; i += THREADS * STEP) v += weights<DT>(pr, qr, i, V);
+        total = block_sum(v, s[0]);
+    } else {
+        const double aim = static_cast<double>(a.u[r0 + kept]) * total;
+        // The first part whose running sum passes, or the last with any weight.
+        const unsigned long long passes = __ballot(run > aim), some = __ballot(part_sum > 0.0);
+        const int pick = uniform(passes ? __builtin_ctzll(passes) : some ? 63 - __builtin_clzll(some) : 0);
+        if (pick > 0) base = __shfl(run, pick - 1, 64);
+        from = pick * a.part;
+        to = from + a.part < V ? from + a.part : V;
+    }
     int token = -1;
-    if (drawn) {
-        const int pick = passes ? __builtin_ctzll(passes) : 63 - __builtin_clzll(some);
-        const double before = pick > 0 ? __shfl(run, pick - 1, 64) : 0.0;
-        const int from = pick * a.chunk, to = from + a.chunk < V ? from + a.chunk : V;
-        double base = before;
+    if (total > 0.0 && total <= 1.7976931348623157e308) {
+        const double aim = static_cast<double>(a.u[r0 + kept]) * total;
         int last = -1;  // the last index with any weight, if none passes
         for (int at = from; at < to; at += THREADS * STEP) {
             double w[STEP], mine = 0.0;
@@ -188,24 +210,24 @@ __global__ __launch_bounds__(THREADS) void k_verify(VerifyArgs a) {
                                   : 0.0;
                 mine += w[j];
             }
-            const double incl = block_scan(mine, s);
+            const double incl = block_scan(mine, s[0]);
             double r = base + (incl - mine);
-            int hit = 0x7FFFFFFF;
+            int hit = NONE;
 #pragma unroll
             for (int j = 0; j < STEP; ++j) {
                 r += w[j];
                 if (w[j] > 0.0) last = i + j;
-                if (hit == 0x7FFFFFFF && w[j] > 0.0 && r > aim) hit = i + j;
+                if (hit == NONE && w[j] > 0.0 && r > aim) hit = i + j;
             }
-            if (hit != 0x7FFFFFFF) atomicMin(&found, hit);
+            if (hit != NONE) atomicMin(&found, hit);
             __syncthreads();
-            if (found != 0x7FFFFFFF) break;
-            if (t == THREADS - 1) s[0] = base + incl;
+            if (found != NONE) break;
+            if (t == THREADS - 1) s[0][0] = base + incl;
             __syncthreads();
-            base = s[0];
+            base = s[0][0];
         }
         token = found;
-        if (token == 0x7FFFFFFF) {
+        if (token == NONE) {
             // Rounding kept the running sum at or below the aim.
             __syncthreads();
             if (t == 0) found = -1;
@@ -223,7 +245,7 @@ __global__ __launch_bounds__(THREADS) void k_verify(VerifyArgs a) {
 }  // namespace
 
 hipError_t launch_verify(const VerifyArgs &a, int dtype, hipStream_t st) {
-    const dim3 grid(a.chunks, a.n_seqs);
+    const dim3 grid((a.parts + a.group - 1) / a.group, a.n_seqs);
     switch (dtype) {
         case DT_F32: k_verify<DT_F32><<<grid, THREADS, 0, st>>>(a); break;
         case DT_F16: k_verify<DT_F16><<<grid, THREADS, 0, st>>>(a); break;

@@ -3,20 +3,23 @@
 // its query rows.
 //
 // In the log2 domain, for one query row over keys t with scores s_t, value
-// exponents b_t (v_t = 2^b_t v8_t) and c = scale * log2(e):
-//     x_t = c s_t + b_t,   m = max x_t,   p_t = 2^(x_t - m)
+// exponents b_t (v_t = 2^b_t v8_t) and c = scale * log2(e), against a whole
+// number m near max(c s_t + b_t):
+//     y_t = c s_t + (b_t - m),   p_t = 2^y_t
 //     O = sum p_t v8_t,    l = sum p_t 2^-b_t,   out = O / l,
 //     lse = ln 2 * (m + log2 l).
 // The value's exponent goes into the weight, so that the values' elements
-// feed the matrix instruction as they are; p_t stays near or below 1 for
-// values of any size and is exact enough in 16 bits.
+// feed the matrix instruction as they are and p_t is near or below 1 for
+// values of any size: exact enough in fp16.  b_t - m is exact, so y_t is
+// rounded once, where it is small.
 //
 // Both products are computed transposed, S^T = K Q^T and O^T = V^T P^T: the
 // keys' rows of S^T come out in the lanes that P^T needs them in, so the
 // weights never leave the registers.  A wave takes 64 keys at a time straight
 // from the cache into registers, 16 bytes a lane; no key is read by two waves
-// of an item.  Each wave keeps m, l and O of its own keys, and the workgroup
-// joins its four at the end.
+// for the same rows.  Each wave keeps m, l and O of its own keys; the four
+// waves of a workgroup either work on one item and join at the end, or each
+// on an item of its own.
 #include "attend_plan.hpp"
 #include "dtype.hpp"
 #include "kv_internal.hpp"
@@ -29,8 +32,8 @@ typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
 constexpr float LN2 = 0.69314718055994530942f;
-// The running maximum is moved only when a score passes it by this much
-// (log2): p stays below 2^8, far inside fp16, and most tiles scale nothing.
+// m is moved only when a y passes it by this much: p stays below 2^8, far
+// inside fp16, and most tiles scale nothing.
 constexpr float SLACK = 8.0f;
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -53,24 +56,55 @@ __device__ __forceinline__ typename Elem<DT>::vec8 widen(uint32_t lo, uint32_t h
     }
 }
 
-__device__ __forceinline__ int byte_of(const u32x4_t &w, int i) { return (w[i / 4] >> (8 * (i % 4))) & 255; }
+__device__ __forceinline__ uint32_t byte_of(const u32x4_t &w, int i) { return (w[i / 4] >> (8 * (i % 4))) & 255u; }
 
-__device__ __forceinline__ float pow2(int byte) { return __uint_as_float(static_cast<uint32_t>(byte) << 23); }
+// 2^(byte - 127) (byte 0: 0).
+__device__ __forceinline__ float pow2(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// The largest of a value held by the lanes r, r + 16, r + 32 and r + 48.
+__device__ __forceinline__ float max_over_g(float v) {
+    v = fmaxf(v, __shfl_xor(v, 16, 64));
+    return fmaxf(v, __shfl_xor(v, 32, 64));
+}
 
 constexpr int lds_floats(int D, int QB) { return ATTEND_WAVES * 16 * QB * (D + 4 + 2); }
 
-// One item for one key/value head, by one workgroup.  QB blocks of 16 query
-// rows; row = token of the item x query head of the key head.
+// Four of a row's elements (d .. d + 3): a partial result, or the output.
+template <int DT, int D>
+__device__ __forceinline__ void emit(const AttendArgs &a, const AttendItem &it, const AttendToken *toks, int i,
+                                     int head, int d, f32x4_t sum, float M, float L) {
+    if (it.part0 >= 0) {
+        const long at = static_cast<long>(it.part0 + i) * a.heads + head;
+        *reinterpret_cast<f32x4_t *>(a.part_o + at * D + d) = sum;
+        if (d == 0) {
+            a.part_ml[at * 2] = M;
+            a.part_ml[at * 2 + 1] = L;
+        }
+        return;
+    }
+    const long at = static_cast<long>(toks[i].token) * a.heads + head;
+    // No key seen: zeros.  (L is NaN, not 0, where a seen key is poisoned.)
+    const float f = L == 0.0f ? 0.0f : 1.0f / L;
+    typename Elem<DT>::raw w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = Elem<DT>::from_f(sum[j] * f);
+    *reinterpret_cast<uint2 *>(a.out + at * D + d) = *reinterpret_cast<const uint2 *>(w);
+    if (d == 0 && a.lse != nullptr) a.lse[at] = LN2 * (M + log2f(L));
+}
+
+// One wave's item for one key/value head.  QB blocks of 16 query rows; row =
+// token of the item x query head of the key head.
 template <int DT, int D, int QB>
 __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendItem &it, const AttendToken *toks,
-                                            const int32_t *page_list, int kvh, float *lds) {
+                                            const int32_t *pages, int kvh, int wave, float *lds) {
     using V8 = typename Elem<DT>::vec8;
     constexpr int NC = D / 64;   // 64-element parts of a key's row: 16 bytes a lane each
     constexpr int NH = D / 16;   // 16-element rows of V^T
     constexpr int ROWS = 16 * QB;
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
     const int r = lane & 15, g = lane >> 4;
-    const int32_t *pages = page_list + it.page0;
+    const bool joined = (it.flags & ATTEND_JOINED) != 0;
+    const int step = joined ? ATTEND_WAVES : 1;
 
     // Queries: lane (r, g) holds row r of each block, elements 64 c + 16 g + 8 h .. + 7.
     V8 qf[QB][2 * NC];
@@ -85,17 +119,19 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
         for (int c = 0; c < NC; ++c)
 #pragma unroll
             for (int h = 0; h < 2; ++h) qf[b][2 * c + h] = load8<V8>(q + c * 64 + g * 16 + h * 8);
-        const int l = it.limit0 + at * it.step;
+        const int l = it.limit0 + ((it.flags & ATTEND_STEP) ? at : 0);
         lim[b] = l < it.end ? l : it.end;
     }
     // Below this every row sees every key.
     const int all = it.limit0 < it.end ? it.limit0 : it.end;
 
-    float m[QB], l[QB];
+    // bm = 127 - m: y = c s + (bm - vinv).  thr: what y must pass to move m.
+    float bm[QB], thr[QB], l[QB];
     f32x4_t o[NH][QB];
 #pragma unroll
     for (int b = 0; b < QB; ++b) {
-        m[b] = -INFINITY;
+        bm[b] = static_cast<float>(KV_EXP_BIAS);
+        thr[b] = -INFINITY;  // until the row has seen a key
         l[b] = 0.0f;
 #pragma unroll
         for (int h = 0; h < NH; ++h) o[h][b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
@@ -108,7 +144,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
     // key 16 (r / 4) + 4 x + r % 4.  Values: lane (r, g) loads element 16 h +
     // r of block g's 16 keys.
     const int t_end = (it.end + ATTEND_TILE - 1) / ATTEND_TILE;
-    int t = it.begin / ATTEND_TILE + wave;
+    int t = it.begin / ATTEND_TILE + (joined ? wave : 0);
     const int last_block = it.end > 0 ? (it.end - 1) / KV_BLOCK : 0;
     const int page_mask = (1 << a.page_shift) - 1;
 
@@ -121,57 +157,54 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
     };
     u32x4_t kw[4][NC], vw[NH], ke, ve;
     auto load_k = [&](long R) {
+        const uint8_t *p = a.k + (R + (r & 3)) * D + g * 16;
 #pragma unroll
         for (int x = 0; x < 4; ++x)
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-                kw[x][c] = *reinterpret_cast<const u32x4_t *>(a.k + (R + 4 * x + (r & 3)) * D + c * 64 + g * 16);
+            for (int c = 0; c < NC; ++c) kw[x][c] = *reinterpret_cast<const u32x4_t *>(p + 4 * x * D + c * 64);
         ke = *reinterpret_cast<const u32x4_t *>(a.kexp + R);
     };
     auto load_v = [&](long R) {
+        const uint8_t *p = a.v + R * D + r * KV_BLOCK;
 #pragma unroll
-        for (int h = 0; h < NH; ++h) vw[h] = *reinterpret_cast<const u32x4_t *>(a.v + R * D + (h * 16 + r) * KV_BLOCK);
-        ve = *reinterpret_cast<const u32x4_t *>(a.vexp + R);
+        for (int h = 0; h < NH; ++h) vw[h] = *reinterpret_cast<const u32x4_t *>(p + h * 16 * KV_BLOCK);
+        ve = *reinterpret_cast<const u32x4_t *>(a.vinv + R);
     };
     long kR = 0, vR = 0;
     if (t < t_end) {
         load_k(block_row(4 * t + (r >> 2)));
         load_v(block_row(4 * t + g));
-        kR = block_row(4 * (t + ATTEND_WAVES) + (r >> 2));
-        vR = block_row(4 * (t + ATTEND_WAVES) + g);
+        kR = block_row(4 * (t + step) + (r >> 2));
+        vR = block_row(4 * (t + step) + g);
     }
 
-    for (; t < t_end; t += ATTEND_WAVES) {
+    for (; t < t_end; t += step) {
         const int key0 = t * ATTEND_TILE;
-        const bool more = t + ATTEND_WAVES < t_end;
+        const bool more = t + step < t_end;
         // Scores.  bf16 holds any element times its scale; fp16 does for
         // keys within 2^-15 of the tile's largest scale, and what is lost of
         // the others is below 2^-24 of the largest, so the tile's scale is
         // taken out of the conversion there.
-        float kscale[4], cs = a.scale;
+        uint32_t kb[4];
+        float cs = a.scale;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const int b = (ke[x] >> (8 * (r & 3))) & 255;
-            kscale[x] = pow2(b);
-            if constexpr (DT == DT_F16) kscale[x] = __uint_as_float(static_cast<uint32_t>(b));
-        }
+        for (int x = 0; x < 4; ++x) kb[x] = (ke[x] >> (8 * (r & 3))) & 255u;
         if constexpr (DT == DT_F16) {
-            int top = 1;
+            uint32_t top = 1;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const int key = key0 + 16 * (r >> 2) + 4 * x + (r & 3);
-                const int b = static_cast<int>(__float_as_uint(kscale[x]));
-                top = key < it.end && b > top ? b : top;
+                top = key < it.end && kb[x] > top ? kb[x] : top;
             }
 #pragma unroll
             for (int d = 1; d < 16; d <<= 1) {
-                const int other = __shfl_xor(top, d, 64);
+                const uint32_t other = __shfl_xor(top, d, 64);
                 top = other > top ? other : top;
             }
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                const int b = static_cast<int>(__float_as_uint(kscale[x])) - top + KV_EXP_BIAS;
-                kscale[x] = pow2(b < 1 ? 1 : b > 254 ? 254 : b);
+                const int e = static_cast<int>(kb[x]) - static_cast<int>(top) + KV_EXP_BIAS;
+                kb[x] = e < 1 ? 1 : e > 254 ? 254 : e;
             }
             cs *= pow2(top);
         }
@@ -184,25 +217,23 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
             for (int c = 0; c < NC; ++c)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const V8 kf = widen<DT>(kw[x][c][2 * h], kw[x][c][2 * h + 1], kscale[x]);
+                    const V8 kf = widen<DT>(kw[x][c][2 * h], kw[x][c][2 * h + 1], pow2(kb[x]));
 #pragma unroll
                     for (int b = 0; b < QB; ++b) s[x][b] = Elem<DT>::mfma(kf, qf[b][2 * c + h], s[x][b]);
                 }
         }
-        if (more) load_k(kR);
+        if (more) {
+            load_k(kR);
+            kR = block_row(4 * (t + 2 * step) + (r >> 2));
+        }
 
-        float be[16], ib[16];
+        float top[QB];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const int b = byte_of(ve, i);
-            be[i] = static_cast<float>(b) - static_cast<float>(KV_EXP_BIAS);
-            // (A poisoned row's is 0: its score is NaN where it is seen, and its weight 0 where not.)
-            ib[i] = pow2(b < 2 * KV_EXP_BIAS ? 2 * KV_EXP_BIAS - b : 0);
+            const float vi = static_cast<float>(byte_of(ve, i));
+#pragma unroll
+            for (int b = 0; b < QB; ++b) s[i / 4][b][i % 4] = fmaf(s[i / 4][b][i % 4], cs, bm[b] - vi);
         }
-#pragma unroll
-        for (int b = 0; b < QB; ++b)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s[i / 4][b][i % 4] = fmaf(s[i / 4][b][i % 4], cs, be[i]);
         if (key0 + ATTEND_TILE > all) {
 #pragma unroll
             for (int b = 0; b < QB; ++b)
@@ -210,25 +241,28 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
                 for (int i = 0; i < 16; ++i)
                     if (key0 + 16 * g + i >= lim[b]) s[i / 4][b][i % 4] = -INFINITY;
         }
-        float top[QB];
         bool moves = false;
 #pragma unroll
         for (int b = 0; b < QB; ++b) {
             float v = s[0][b][0];
 #pragma unroll
             for (int i = 1; i < 16; ++i) v = fmaxf(v, s[i / 4][b][i % 4]);
-            v = fmaxf(v, __shfl_xor(v, 16, 64));
-            v = fmaxf(v, __shfl_xor(v, 32, 64));
-            top[b] = v;
-            moves |= v > m[b] + SLACK;
+            top[b] = max_over_g(v);
+            moves |= top[b] > thr[b];
         }
         if (__any(moves)) {
 #pragma unroll
             for (int b = 0; b < QB; ++b) {
-                const float to = fmaxf(m[b], top[b]);
-                const float f = to == m[b] ? 1.0f : exp2_fast(m[b] - to);
-                m[b] = to;
+                // Whole steps; a row with no key yet, or with an infinite score, stays.
+                const float up = ceilf(top[b]);
+                const bool move = top[b] > thr[b] && fabsf(up) < INFINITY;
+                const float d = move ? up : 0.0f;
+                const float f = move && thr[b] > 0.0f ? exp2_fast(-d) : 1.0f;
+                thr[b] = move ? SLACK : thr[b];
+                bm[b] -= d;
                 l[b] *= f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[i / 4][b][i % 4] -= d;
 #pragma unroll
                 for (int h = 0; h < NH; ++h)
 #pragma unroll
@@ -238,18 +272,14 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
         // Weights, 8 keys an operand: half x holds keys 8 x .. 8 x + 7 of the lane's 16.
         f16x8_t p[2][QB];
 #pragma unroll
-        for (int b = 0; b < QB; ++b) {
-            const float ref = m[b] == -INFINITY ? 0.0f : m[b];
+        for (int i = 0; i < 16; ++i) {
+            const float ib = pow2(byte_of(ve, i));
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float w = exp2_fast(s[i / 4][b][i % 4] - ref);
-                l[b] = fmaf(w, ib[i], l[b]);
+            for (int b = 0; b < QB; ++b) {
+                const float w = exp2_fast(s[i / 4][b][i % 4]);
+                l[b] = fmaf(w, ib, l[b]);
                 p[i / 8][b][i % 8] = static_cast<_Float16>(w);
             }
-        }
-        if (more) {
-            const int next = t + 2 * ATTEND_WAVES;
-            kR = block_row(4 * next + (r >> 2));
         }
 #pragma unroll
         for (int h = 0; h < NH; ++h)
@@ -261,16 +291,35 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
             }
         if (more) {
             load_v(vR);
-            vR = block_row(4 * (t + 2 * ATTEND_WAVES) + g);
+            vR = block_row(4 * (t + 2 * step) + g);
         }
+    }
+
+    float m[QB];
+#pragma unroll
+    for (int b = 0; b < QB; ++b) {
+        l[b] += __shfl_xor(l[b], 16, 64);
+        l[b] += __shfl_xor(l[b], 32, 64);
+        m[b] = thr[b] > 0.0f ? static_cast<float>(KV_EXP_BIAS) - bm[b] : -INFINITY;
+        // NaN stays in l even where no finite score has moved m.
+        if (l[b] != l[b]) m[b] = l[b];
+    }
+    if (!joined) {
+#pragma unroll
+        for (int b = 0; b < QB; ++b) {
+            const int row = b * 16 + r, i = row / a.gq;
+            if (i < it.n_tok)
+#pragma unroll
+                for (int h = 0; h < NH; ++h)
+                    emit<DT, D>(a, it, toks, i, kvh * a.gq + row - i * a.gq, h * 16 + g * 4, o[h][b], m[b], l[b]);
+        }
+        return;
     }
 
     // Join the four waves: O scaled to the workgroup's maximum, added in LDS.
     float *lo = lds, *lm = lds + ATTEND_WAVES * ROWS * (D + 4);
 #pragma unroll
     for (int b = 0; b < QB; ++b) {
-        l[b] += __shfl_xor(l[b], 16, 64);
-        l[b] += __shfl_xor(l[b], 32, 64);
         if (g == 0) {
             lm[(wave * ROWS + b * 16 + r) * 2] = m[b];
             lm[(wave * ROWS + b * 16 + r) * 2 + 1] = l[b];
@@ -298,24 +347,8 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
             L = fmaf(f, lm[(w * ROWS + row) * 2 + 1], L);
             sum += f * *reinterpret_cast<const f32x4_t *>(lo + (w * ROWS + row) * (D + 4) + d);
         }
-        const int i = row / a.gq, head = kvh * a.gq + row - i * a.gq;
-        if (it.part0 >= 0) {
-            const long at_part = static_cast<long>(it.part0 + i) * a.heads + head;
-            *reinterpret_cast<f32x4_t *>(a.part_o + at_part * D + d) = sum;
-            if (d == 0) {
-                a.part_ml[at_part * 2] = M;
-                a.part_ml[at_part * 2 + 1] = L;
-            }
-        } else {
-            const long at_out = static_cast<long>(toks[i].token) * a.heads + head;
-            // No key seen: zeros.  (L is NaN, not 0, where a seen key is poisoned.)
-            const float f = L == 0.0f ? 0.0f : 1.0f / L;
-            typename Elem<DT>::raw w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = Elem<DT>::from_f(sum[j] * f);
-            *reinterpret_cast<uint2 *>(a.out + at_out * D + d) = *reinterpret_cast<const uint2 *>(w);
-            if (d == 0 && a.lse != nullptr) a.lse[at_out] = LN2 * (M + log2f(L));
-        }
+        const int i = row / a.gq;
+        emit<DT, D>(a, it, toks, i, kvh * a.gq + row - i * a.gq, d, sum, M, L);
     }
     __syncthreads();  // the next item writes LDS again
 }
@@ -334,16 +367,17 @@ __global__ __launch_bounds__(256, 2) void k_attend(AttendArgs a) {
     const AttendItem *items = reinterpret_cast<const AttendItem *>(a.meta + sizeof(AttendHeader));
     const AttendToken *toks = reinterpret_cast<const AttendToken *>(a.meta + h->token_off);
     const int32_t *pages = reinterpret_cast<const int32_t *>(a.meta + h->page_off);
-    const int n = plan_fits(a, h) ? h->n_items * a.kv_heads : 0;
-    // The grid has a workgroup for each item of the plan at launch; a graph
+    const int n = plan_fits(a, h) ? h->n_groups * a.kv_heads : 0;
+    const int wave = uniform(threadIdx.x >> 6);
+    // The grid has a workgroup for each of the plan's at launch; a graph
     // replayed after a new plan may find more.
     for (int w = blockIdx.x; w < n; w += gridDim.x) {
         const int i = w / a.kv_heads, kvh = w - i * a.kv_heads;
-        const AttendItem it = items[i];
-        if (it.n_tok * a.gq <= 16)
-            attend_item<DT, D, 1>(a, it, toks + it.tok0, pages, kvh, lds);
-        else
-            attend_item<DT, D, 2>(a, it, toks + it.tok0, pages, kvh, lds);
+        const AttendItem it = items[i * ATTEND_WAVES + wave];
+        if (it.n_tok * a.gq > 16)
+            attend_item<DT, D, 2>(a, it, toks + it.tok0, pages + it.page0, kvh, wave, lds);
+        else if (it.n_tok > 0)
+            attend_item<DT, D, 1>(a, it, toks + it.tok0, pages + it.page0, kvh, wave, lds);
     }
 }
 
@@ -386,13 +420,13 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
 }
 
 template <int DT, int D>
-hipError_t run(const AttendArgs &a, int n_items, int n_tokens, hipStream_t st) {
+hipError_t run(const AttendArgs &a, int n_groups, int n_tokens, hipStream_t st) {
     constexpr size_t lds = lds_floats(D, ATTEND_ROWS / 16) * sizeof(float);
     static const hipError_t set = hipFuncSetAttribute(reinterpret_cast<const void *>(k_attend<DT, D>),
                                                       hipFuncAttributeMaxDynamicSharedMemorySize,
                                                       static_cast<int>(lds));
     if (set != hipSuccess) return set;
-    const long wgs = static_cast<long>(n_items) * a.kv_heads;
+    const long wgs = static_cast<long>(n_groups) * a.kv_heads;
     k_attend<DT, D><<<static_cast<unsigned>(wgs < 1 ? 1 : wgs > 65536 ? 65536 : wgs), 256, lds, st>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -404,10 +438,10 @@ hipError_t run(const AttendArgs &a, int n_items, int n_tokens, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_attend(const AttendArgs &a, int dtype, int dim, int n_items, int n_tokens, hipStream_t st) {
+hipError_t launch_attend(const AttendArgs &a, int dtype, int dim, int n_groups, int n_tokens, hipStream_t st) {
     if (dtype == DT_F16)
-        return dim == 128 ? run<DT_F16, 128>(a, n_items, n_tokens, st) : run<DT_F16, 64>(a, n_items, n_tokens, st);
-    return dim == 128 ? run<DT_BF16, 128>(a, n_items, n_tokens, st) : run<DT_BF16, 64>(a, n_items, n_tokens, st);
+        return dim == 128 ? run<DT_F16, 128>(a, n_groups, n_tokens, st) : run<DT_F16, 64>(a, n_groups, n_tokens, st);
+    return dim == 128 ? run<DT_BF16, 128>(a, n_groups, n_tokens, st) : run<DT_BF16, 64>(a, n_groups, n_tokens, st);
 }
 
 }  // namespace lora

@@ -30,13 +30,15 @@ AttendPlanner::AttendPlanner(int max_seqs, int max_groups, int max_tokens, int m
     const int gq = n_heads / n_kv_heads;
     // A block has at least one token, of one sequence or of one group.
     max_spans_ = 2 * max_tokens;
-    // plan() gives a span ceil(cost / target) items and the targets sum to
-    // ATTEND_SLOTS / n_kv_heads over all spans.
-    const int extra = ceil_div(ATTEND_SLOTS, n_kv_heads) + 1;
-    max_items_ = max_spans_ + extra;
-    // Every span's tokens once, and a block's tokens for each further item.
+    // plan() gives a span of more than one wave's share ceil(share / 4)
+    // workgroups, and the shares sum to ATTEND_SLOTS / n_kv_heads.
+    const int extra = ceil_div(ATTEND_SLOTS / ATTEND_WAVES, n_kv_heads) + 1;
+    max_groups_wg_ = max_spans_ + extra;
+    // Every span's tokens once, and a block's tokens for each further workgroup.
     max_part_rows_ = 2 * max_tokens + extra * attend_block_tokens(gq);
-    items_.reserve(static_cast<size_t>(max_items_));
+    items_.reserve(static_cast<size_t>(max_groups_wg_) * ATTEND_WAVES);
+    whole_.reserve(static_cast<size_t>(max_groups_wg_));
+    single_.reserve(static_cast<size_t>(max_spans_));
     tokens_.reserve(static_cast<size_t>(max_tokens));
     pages_.reserve(static_cast<size_t>(max_pages) + 1);
     spans_.reserve(static_cast<size_t>(max_spans_));
@@ -48,12 +50,14 @@ AttendPlanner::AttendPlanner(int max_seqs, int max_groups, int max_tokens, int m
 }
 
 size_t AttendPlanner::max_bytes() const {
-    return sizeof(AttendHeader) + static_cast<size_t>(max_items_) * sizeof(AttendItem) +
+    return sizeof(AttendHeader) + static_cast<size_t>(max_groups_wg_) * ATTEND_WAVES * sizeof(AttendItem) +
            static_cast<size_t>(max_tokens_) * sizeof(AttendToken) + (static_cast<size_t>(max_pages_) + 4) * 4;
 }
 
 void AttendPlanner::clear() {
     items_.clear();
+    whole_.clear();
+    single_.clear();
     tokens_.clear();
     pages_.clear();
     spans_.clear();
@@ -159,28 +163,29 @@ int AttendPlanner::plan(const AttendBatch &b, const AttendGeometry &geo) {
         }
     }
 
-    // Each item costs about an even share of the whole, four tiles at least
-    // (one for each wave).
-    const int64_t target =
-        std::max<int64_t>((cost * n_kv_heads_ + ATTEND_SLOTS - 1) / ATTEND_SLOTS, ATTEND_WAVES * tile_cost(1));
+    // A wave's share of the whole, a tile at least.  A span of up to one share
+    // goes to one wave: its loop is as long as it can be for what it costs to
+    // begin and end.  Longer ones go to whole workgroups, whose waves take
+    // alternating tiles and join in LDS.
+    const int64_t share = std::max<int64_t>((cost * n_kv_heads_ + ATTEND_SLOTS - 1) / ATTEND_SLOTS, tile_cost(1));
     for (Span &s : spans_) {
-        const int tiles = ceil_div(s.end, ATTEND_TILE);
-        const int64_t c = static_cast<int64_t>(tiles) * tile_cost(s.n_tok * gq);
-        s.splits = static_cast<int>(
-            std::max<int64_t>(1, std::min<int64_t>((c + target - 1) / target, ceil_div(tiles, ATTEND_WAVES))));
-        for (int i = 0; i < s.n_tok; ++i) tokens_[static_cast<size_t>(s.tok0 + i)].n[s.own] = s.splits;
+        const int64_t c = static_cast<int64_t>(ceil_div(s.end, ATTEND_TILE)) * tile_cost(s.n_tok * gq);
+        s.splits = c <= share ? 0 : static_cast<int>((c + ATTEND_WAVES * share - 1) / (ATTEND_WAVES * share));
+        for (int i = 0; i < s.n_tok; ++i) tokens_[static_cast<size_t>(s.tok0 + i)].n[s.own] = std::max(1, s.splits);
     }
     for (Span &s : spans_) {
         // Alone: no token of the block has a result of another item.
-        bool alone = s.splits == 1;
+        bool alone = s.splits <= 1;
         for (int i = 0; alone && i < s.n_tok; ++i) alone = tokens_[static_cast<size_t>(s.tok0 + i)].n[!s.own] == 0;
-        const int tiles = ceil_div(s.end, ATTEND_TILE);
+        const int tiles = ceil_div(s.end, ATTEND_TILE), splits = std::max(1, s.splits);
         const int base = part_rows_;
-        for (int k = 0; k < s.splits; ++k) {
-            const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * k / s.splits);
-            const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (k + 1) / s.splits);
-            items_.push_back(AttendItem{s.tok0, s.n_tok, s.page0, t0 * ATTEND_TILE, std::min(s.end, t1 * ATTEND_TILE),
-                                        s.limit0, s.step, alone ? -1 : base + k * s.n_tok});
+        for (int k = 0; k < splits; ++k) {
+            const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * k / splits);
+            const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (k + 1) / splits);
+            (s.splits > 0 ? whole_ : single_)
+                .push_back(AttendItem{s.tok0, s.n_tok, s.page0, t0 * ATTEND_TILE, std::min(s.end, t1 * ATTEND_TILE),
+                                      s.limit0, (s.step ? ATTEND_STEP : 0) | (s.splits > 0 ? ATTEND_JOINED : 0),
+                                      alone ? -1 : base + k * s.n_tok});
         }
         for (int i = 0; i < s.n_tok; ++i) {
             AttendToken &t = tokens_[static_cast<size_t>(s.tok0 + i)];
@@ -191,27 +196,33 @@ int AttendPlanner::plan(const AttendBatch &b, const AttendGeometry &geo) {
                 t.stride[s.own] = s.n_tok;
             }
         }
-        if (!alone) part_rows_ += s.splits * s.n_tok;
+        if (!alone) part_rows_ += splits * s.n_tok;
     }
     for (AttendToken &t : tokens_) {
         if (t.pad) t.n[0] = t.n[1] = 0;
         t.pad = 0;
         n_split_ += t.n[0] + t.n[1] > 0;
     }
-    // The dearest first: what is left at the end is short.
-    std::sort(items_.begin(), items_.end(), [gq](const AttendItem &x, const AttendItem &y) {
+    // The dearest first, so that what is left at the end is short and the four
+    // waves of a workgroup end together.
+    auto dearer = [gq](const AttendItem &x, const AttendItem &y) {
         const int64_t cx = static_cast<int64_t>(x.end - x.begin) * tile_cost(x.n_tok * gq);
         const int64_t cy = static_cast<int64_t>(y.end - y.begin) * tile_cost(y.n_tok * gq);
         if (cx != cy) return cx > cy;
         if (x.tok0 != y.tok0) return x.tok0 < y.tok0;
         return x.page0 != y.page0 ? x.page0 < y.page0 : x.begin < y.begin;
-    });
+    };
+    std::sort(whole_.begin(), whole_.end(), dearer);
+    std::sort(single_.begin(), single_.end(), dearer);
+    for (const AttendItem &it : whole_) items_.insert(items_.end(), ATTEND_WAVES, it);
+    items_.insert(items_.end(), single_.begin(), single_.end());
+    while (items_.size() % ATTEND_WAVES != 0) items_.push_back(AttendItem{});
     return LORA_OK;
 }
 
 size_t AttendPlanner::write(void *to) const {
     AttendHeader h{};
-    h.n_items = static_cast<int32_t>(items_.size());
+    h.n_groups = groups();
     h.n_tokens = static_cast<int32_t>(tokens_.size());
     h.n_split = n_split_;
     h.page_size = page_size_;

@@ -16,17 +16,20 @@
 
 namespace lora {
 
-// One work item: the query tokens sorted at tok0 .. tok0 + n_tok - 1 over the
-// keys begin .. end - 1 of the span whose pages start at page0.  Query token
-// tok0 + i sees keys below min(end, limit0 + i * step).
+// One wave's work: the query tokens sorted at tok0 .. tok0 + n_tok - 1 (none:
+// the wave idles) over the keys begin .. end - 1 of the span whose pages start
+// at page0, or over every fourth tile of them where the workgroup's four waves
+// are joined.  Query token tok0 + i sees keys below min(end, limit0 + i * step).
 struct AttendItem {
     int32_t tok0, n_tok;
     int32_t page0;
     int32_t begin, end;
-    int32_t limit0, step;
+    int32_t limit0;
+    int32_t flags;  // bit 0: step; bit 1: the four waves share this item
     int32_t part0;  // partial results of token i go to row part0 + i; -1: no other item has this token
 };
 static_assert(sizeof(AttendItem) == 32, "read by the kernels as two 16-byte words");
+enum : int32_t { ATTEND_STEP = 1, ATTEND_JOINED = 2 };
 
 // One sorted query token: its row in q and out, and where its partial results
 // are: rows part[k] + j * stride[k], j < n[k] (k = 0 the prefix, 1 its own).
@@ -37,9 +40,10 @@ struct AttendToken {
 };
 static_assert(sizeof(AttendToken) == 32, "read by the kernels as two 16-byte words");
 
-// What the kernels read first.  Offsets in bytes from the header.
+// What the kernels read first.  Offsets in bytes from the header; a workgroup
+// (for one key/value head) has four items, one for each wave.
 struct AttendHeader {
-    int32_t n_items, n_tokens, n_split;  // n_split: tokens with partial results
+    int32_t n_groups, n_tokens, n_split;  // n_split: tokens with partial results
     int32_t token_off, page_off;
     int32_t page_size, n_pages;         // of the caches it is for
     int32_t pad[9];
@@ -47,12 +51,12 @@ struct AttendHeader {
 static_assert(sizeof(AttendHeader) == 64, "items follow at byte 64");
 
 constexpr int ATTEND_TILE = 64;       // keys a wave takes at a time
-constexpr int ATTEND_WAVES = 4;       // waves of a workgroup, on alternating tiles
+constexpr int ATTEND_WAVES = 4;       // waves of a workgroup
 constexpr int ATTEND_MAX_GQ = 32;     // query heads per key/value head
 constexpr int ATTEND_MAX_KEYS = 1 << 30;  // keys of one sequence or prefix (tiles times 64 stay whole 32-bit numbers)
 constexpr int ATTEND_ROWS = 32;       // query rows (tokens x heads of a key head) of an item
-// Workgroups the items are cut for: two on each of the 256 CUs.
-constexpr int ATTEND_SLOTS = 512;
+// Waves the work is cut for: two workgroups on each of the 256 CUs.
+constexpr int ATTEND_SLOTS = 2048;
 
 // Query tokens of one item, for gq query heads per key/value head.
 inline int attend_block_tokens(int gq) { return gq >= ATTEND_ROWS ? 1 : ATTEND_ROWS / gq; }
@@ -87,7 +91,8 @@ public:
     // The bytes the device reads, max_bytes() at most; returns how many.
     size_t write(void *to) const;
 
-    const std::vector<AttendItem> &items() const { return items_; }
+    const std::vector<AttendItem> &items() const { return items_; }  // four a workgroup
+    int groups() const { return static_cast<int>(items_.size()) / ATTEND_WAVES; }
     const std::vector<AttendToken> &tokens() const { return tokens_; }
     const std::vector<int32_t> &pages() const { return pages_; }
     int part_rows() const { return part_rows_; }
@@ -97,14 +102,14 @@ private:
     struct Span {
         int tok0, n_tok, page0, end, limit0, step;
         bool own;
-        int splits;
+        int splits;   // workgroups; 0: one wave
     };
     int check(const AttendBatch &b, const AttendGeometry &geo) const;
     void clear();
 
     int max_seqs_, max_groups_, max_tokens_, max_pages_, n_heads_, n_kv_heads_;
-    int max_spans_, max_items_, max_part_rows_;
-    std::vector<AttendItem> items_;
+    int max_spans_, max_groups_wg_, max_part_rows_;
+    std::vector<AttendItem> items_, whole_, single_;
     std::vector<AttendToken> tokens_;
     std::vector<int32_t> pages_;
     std::vector<Span> spans_;

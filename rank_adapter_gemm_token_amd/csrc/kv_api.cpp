@@ -112,7 +112,8 @@ int lora_kv_create(int n_pages, int page_size, int n_kv_heads, int head_dim, lor
                           n_pages, shift, n_kv_heads, head_dim, static_cast<int>(dtype)};
     // A row that was never written is a row of zeros.
     e = hipMemset(kv->mem, 0, total);
-    if (e == hipSuccess) e = hipMemset(kv->c.kexp, lora::KV_EXP_BIAS + lora::KV_MIN_EXP, 2 * exps);
+    if (e == hipSuccess) e = hipMemset(kv->c.kexp, lora::KV_EXP_BIAS + lora::KV_MIN_EXP, exps);
+    if (e == hipSuccess) e = hipMemset(kv->c.vinv, lora::KV_EXP_BIAS - lora::KV_MIN_EXP, exps);
     if (e == hipSuccess) e = hipDeviceSynchronize();
     if (e != hipSuccess) {
         const int rc = hip_fail(e);
@@ -274,7 +275,7 @@ int lora_attend(lora_kv kv, lora_attend_plan plan, const void *q, int64_t q_stri
     a.k = kv->c.k;
     a.v = kv->c.v;
     a.kexp = kv->c.kexp;
-    a.vexp = kv->c.vexp;
+    a.vinv = kv->c.vinv;
     a.q = static_cast<const uint16_t *>(q);
     a.q_stride = q_stride;
     a.out = static_cast<uint16_t *>(out);
@@ -287,8 +288,8 @@ int lora_attend(lora_kv kv, lora_attend_plan plan, const void *q, int64_t q_stri
     a.page_shift = kv->c.page_shift;
     a.n_pages = kv->c.n_pages;
     a.scale = scale * 1.44269504088896340736f;
-    HIP_TRY(lora::launch_attend(a, kv->c.dtype, plan->head_dim, static_cast<int>(plan->planner.items().size()),
-                                n_tokens, static_cast<hipStream_t>(stream)));
+    HIP_TRY(lora::launch_attend(a, kv->c.dtype, plan->head_dim, plan->planner.groups(), n_tokens,
+                                static_cast<hipStream_t>(stream)));
     return LORA_OK;
 }
 

@@ -161,7 +161,7 @@ __global__ __launch_bounds__(256) void k_kv_write(KvCache c, const uint16_t *k, 
         for (int i = 0; i < N / 4; ++i) kd[i] = kw[i];
         if (l == 0) {
             c.kexp[R] = static_cast<uint8_t>(kb);
-            c.vexp[R] = static_cast<uint8_t>(poison ? KV_POISON : vb);
+            c.vinv[R] = static_cast<uint8_t>(poison ? KV_POISON : 2 * KV_EXP_BIAS - vb);
         }
     };
 
@@ -234,23 +234,23 @@ __global__ __launch_bounds__(256) void k_kv_read(KvCache c, const int32_t *slots
             put(v, token, w, 0, true);
         } else {
             const long R = row_of(c, tile.slot, head);
-            const int vb = c.vexp[R];
-            keys(token, R, vb == KV_POISON);
+            const int vi = c.vinv[R];
+            keys(token, R, vi == KV_POISON);
             const uint8_t *vs = c.v + (R & ~15L) * D + (R & 15) + l * N * KV_BLOCK;
 #pragma unroll
             for (int i = 0; i < N; ++i) w[i / 4] |= static_cast<uint32_t>(vs[i * KV_BLOCK]) << (8 * (i % 4));
-            put(v, token, w, vb, vb == KV_POISON);
+            put(v, token, w, 2 * KV_EXP_BIAS - vi, vi == KV_POISON);
         }
     }
     if (tile.lead < 0) return;
     const int token = first + tile.lead + me;
     const long R = row_of(c, s[15 + tile.lead] + me, head);
-    const int vb = c.vexp[R];
+    const int vi = c.vinv[R];
     const int at = threadIdx.x * N, d = at / KV_BLOCK, part = at % KV_BLOCK;
     uint32_t w[N / 4];
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) w[i] = reinterpret_cast<const uint32_t *>(c.v + (R & ~15L) * D + at)[i];
-    keys(token, R, vb == KV_POISON);
+    keys(token, R, vi == KV_POISON);
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) *reinterpret_cast<uint32_t *>(turned + d * VT_LD + part + 4 * i) = w[i];
     __syncthreads();
@@ -258,7 +258,7 @@ __global__ __launch_bounds__(256) void k_kv_read(KvCache c, const int32_t *slots
     for (int i = 0; i < N / 4; ++i) w[i] = 0u;
 #pragma unroll
     for (int i = 0; i < N; ++i) w[i / 4] |= static_cast<uint32_t>(turned[(l * N + i) * VT_LD + me]) << (8 * (i % 4));
-    put(v, token, w, vb, vb == KV_POISON);
+    put(v, token, w, 2 * KV_EXP_BIAS - vi, vi == KV_POISON);
 }
 
 template <int DT, int D>

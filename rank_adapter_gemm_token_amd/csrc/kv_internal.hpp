@@ -17,18 +17,19 @@ namespace lora {
 //   values  blocks of 16 rows are stored by element: element d of row R at
 //           byte (R - R % 16) * D + d * 16 + R % 16, so that the attention
 //           reads 16 keys' values of one element as one word
-//   kexp, vexp  the exponent bytes, one a row
+//   kexp, vinv  exponent bytes, one a row: a key's b, a value's 254 - b, of
+//           which the attention makes 2^-s by a shift
 // Elements are finite, except that a row whose key or value has a value that
 // is not finite is POISONED: its key elements are NaN (its scores are then
 // NaN, wherever they are looked at, and nothing else is), its value elements
-// 0 and its vexp KV_POISON.
+// 0 and its vinv KV_POISON.
 constexpr int KV_BLOCK = 16;        // rows of a block of values
-constexpr int KV_POISON = 255;
+constexpr int KV_POISON = 0;        // as a float's exponent bits: 0, which no weight of 0 makes NaN
 constexpr int KV_EXP_BIAS = 127;
 constexpr int KV_MIN_EXP = -64;     // least exponent kept: smaller values go to 0
 
 struct KvCache {
-    uint8_t *k, *v, *kexp, *vexp;
+    uint8_t *k, *v, *kexp, *vinv;
     unsigned long long *err;
     int n_pages, page_shift, heads, dim;  // page_size = 1 << page_shift
     int dtype;
@@ -40,7 +41,7 @@ hipError_t launch_kv_read(const KvCache &c, const int32_t *slots, int n_tokens, 
 
 struct AttendArgs {
     const char *meta;      // AttendHeader, items, tokens, pages
-    const uint8_t *k, *v, *kexp, *vexp;
+    const uint8_t *k, *v, *kexp, *vinv;
     const uint16_t *q;
     int64_t q_stride;      // elements from one token's heads to the next's
     uint16_t *out;         // [tokens][heads][dim]
@@ -51,7 +52,7 @@ struct AttendArgs {
     float scale;           // softmax scale times log2(e)
 };
 
-hipError_t launch_attend(const AttendArgs &a, int dtype, int dim, int n_items, int n_tokens, hipStream_t st);
+hipError_t launch_attend(const AttendArgs &a, int dtype, int dim, int n_groups, int n_tokens, hipStream_t st);
 
 struct VerifyArgs {
     const void *p, *q;

@@ -44,7 +44,16 @@ static void check_plan(const AttendPlanner &p, const Lists &b, int heads, int kv
     std::vector<std::vector<char>> pre(seq_of.size()), own(seq_of.size());
     std::vector<int> direct(seq_of.size(), 0);
     std::map<int, int> part_owner;
-    for (const AttendItem &it : p.items()) {
+    CHECK(p.items().size() % ATTEND_WAVES == 0);
+    for (size_t n = 0; n < p.items().size(); ++n) {
+        const AttendItem &it = p.items()[n];
+        const AttendItem &first = p.items()[n - n % ATTEND_WAVES];
+        CHECK((it.flags & ATTEND_JOINED) == (first.flags & ATTEND_JOINED) || it.n_tok == 0);
+        if (it.flags & ATTEND_JOINED) {
+            CHECK(std::memcmp(&it, &first, sizeof it) == 0);
+            if (n % ATTEND_WAVES != 0) continue;  // the four waves share one item
+        }
+        if (it.n_tok == 0) continue;  // nothing for this wave
         CHECK(it.n_tok >= 1 && it.n_tok <= attend_block_tokens(gq) && it.n_tok * gq <= ATTEND_ROWS);
         CHECK(it.begin % ATTEND_TILE == 0 && it.begin <= it.end);
         for (int i = 0; i < it.n_tok; ++i) {
@@ -56,14 +65,14 @@ static void check_plan(const AttendPlanner &p, const Lists &b, int heads, int kv
                 ++direct[static_cast<size_t>(sorted)];
             else
                 CHECK(part_owner.insert({it.part0 + i, sorted}).second && it.part0 + i < p.part_rows());
-            const bool is_prefix = it.step == 0;
+            const bool is_prefix = (it.flags & ATTEND_STEP) == 0;
             const int len = is_prefix ? b.plen[static_cast<size_t>(g)] : b.kv[static_cast<size_t>(s)];
             const int32_t *list = is_prefix ? &b.ppages[static_cast<size_t>(b.ppage0[static_cast<size_t>(g)])]
                                             : b.pages.data() + b.page0[static_cast<size_t>(s)];
             const int seen = is_prefix ? len : len - b.q[static_cast<size_t>(s)] + pos[static_cast<size_t>(t.token)] + 1;
             auto &mine = (is_prefix ? pre : own)[static_cast<size_t>(sorted)];
             mine.resize(static_cast<size_t>(len), 0);
-            const int lim = std::min(it.end, it.limit0 + i * it.step);
+            const int lim = std::min(it.end, it.limit0 + (is_prefix ? 0 : i));
             CHECK(it.end <= len);
             for (int k = it.begin; k < it.end; ++k) {
                 CHECK(p.pages()[static_cast<size_t>(it.page0 + k / page)] == list[k / page]);
@@ -97,7 +106,7 @@ static void check_plan(const AttendPlanner &p, const Lists &b, int heads, int kv
     CHECK(n <= p.max_bytes());
     AttendHeader h;
     std::memcpy(&h, buf.data(), sizeof h);
-    CHECK(h.n_items == (int)p.items().size() && h.n_tokens == (int)p.tokens().size() && h.n_split == split);
+    CHECK(h.n_groups == p.groups() && h.n_tokens == (int)p.tokens().size() && h.n_split == split);
     CHECK(h.page_size == page);
     CHECK(std::memcmp(buf.data() + sizeof h, p.items().data(), p.items().size() * sizeof(AttendItem)) == 0);
 }

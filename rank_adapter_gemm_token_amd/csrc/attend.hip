@@ -106,8 +106,11 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
     const bool joined = (it.flags & ATTEND_JOINED) != 0;
     const int step = joined ? ATTEND_WAVES : 1;
 
-    // Queries: lane (r, g) holds row r of each block, elements 64 c + 16 g + 8 h .. + 7.
-    V8 qf[QB][2 * NC];
+    // Queries: lane (r, g) holds row r of each block, elements 64 c + 16 g + 8
+    // h .. + 7, in LDS (16 bytes a lane): in registers they would push the
+    // loop over 256 and its spills would wait for the prefetch.  The wave's
+    // part of LDS is its own until the join.
+    u32x4_t *qf = reinterpret_cast<u32x4_t *>(lds + wave * ROWS * (D + 4)) + lane;
     int lim[QB];  // keys the row sees
 #pragma unroll
     for (int b = 0; b < QB; ++b) {
@@ -118,7 +121,8 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) qf[b][2 * c + h] = load8<V8>(q + c * 64 + g * 16 + h * 8);
+            for (int h = 0; h < 2; ++h)
+                qf[(b * 2 * NC + 2 * c + h) * 64] = *reinterpret_cast<const u32x4_t *>(q + c * 64 + g * 16 + h * 8);
         const int l = it.limit0 + ((it.flags & ATTEND_STEP) ? at : 0);
         lim[b] = l < it.end ? l : it.end;
     }
@@ -148,13 +152,21 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
     const int last_block = it.end > 0 ? (it.end - 1) / KV_BLOCK : 0;
     const int page_mask = (1 << a.page_shift) - 1;
 
-    // First row of the 16 rows of block `blk` (blocks past the end: the last one).
-    auto block_row = [&](int blk) {
+    // The 16 rows of block `blk` of keys (past the end: the last one): their
+    // page's number, and with that their first row.
+    auto block_page = [&](int blk) {
         blk = blk < last_block ? blk : last_block;
-        const int key = blk * KV_BLOCK;
-        const long page = pages[key >> a.page_shift];
-        return ((page * a.kv_heads + kvh) << a.page_shift) + (key & page_mask);
+        return pages[(blk * KV_BLOCK) >> a.page_shift];
     };
+    auto block_row = [&](int blk, int page) {
+        blk = blk < last_block ? blk : last_block;
+        return ((static_cast<long>(page) * a.kv_heads + kvh) << a.page_shift) + ((blk * KV_BLOCK) & page_mask);
+    };
+    // Loads return in the order of their issue.  A tile's keys and exponents
+    // are issued one tile ahead, after the scores of the tile before, its
+    // values after that tile's second product; the pages of the tile after
+    // that are looked up between the two, and first looked at when they are
+    // needed, so that no wait for one of these covers a later one.  Past the last tile they read its last block again.
     u32x4_t kw[4][NC], vw[NH], ke, ve;
     auto load_k = [&](long R) {
         const uint8_t *p = a.k + (R + (r & 3)) * D + g * 16;
@@ -168,19 +180,25 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
         const uint8_t *p = a.v + R * D + r * KV_BLOCK;
 #pragma unroll
         for (int h = 0; h < NH; ++h) vw[h] = *reinterpret_cast<const u32x4_t *>(p + h * 16 * KV_BLOCK);
-        ve = *reinterpret_cast<const u32x4_t *>(a.vinv + R);
     };
-    long kR = 0, vR = 0;
+    int kp = 0, vp = 0;
     if (t < t_end) {
-        load_k(block_row(4 * t + (r >> 2)));
-        load_v(block_row(4 * t + g));
-        kR = block_row(4 * (t + step) + (r >> 2));
-        vR = block_row(4 * (t + step) + g);
+        const int kb0 = 4 * t + (r >> 2), vb0 = 4 * t + g;
+        kp = block_page(kb0);
+        vp = block_page(vb0);
+        const long vR = block_row(vb0, vp);
+        load_k(block_row(kb0, kp));
+        ve = *reinterpret_cast<const u32x4_t *>(a.vinv + vR);
+        kp = block_page(kb0 + 4 * step);
+        vp = block_page(vb0 + 4 * step);
+        __builtin_amdgcn_sched_barrier(0);
+        load_v(vR);
+        __builtin_amdgcn_sched_barrier(0);
     }
 
     for (; t < t_end; t += step) {
+        asm volatile("" ::: "memory");  // the queries are read again, not kept
         const int key0 = t * ATTEND_TILE;
-        const bool more = t + step < t_end;
         // Scores.  bf16 holds any element times its scale; fp16 does for
         // keys within 2^-15 of the tile's largest scale, and what is lost of
         // the others is below 2^-24 of the largest, so the tile's scale is
@@ -210,31 +228,42 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
         }
         f32x4_t s[4][QB];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
+        for (int x = 0; x < 4; ++x)
 #pragma unroll
             for (int b = 0; b < QB; ++b) s[x][b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < 2; ++h) {
+                V8 qv[QB];
+#pragma unroll
+                for (int b = 0; b < QB; ++b) qv[b] = __builtin_bit_cast(V8, qf[(b * 2 * NC + 2 * c + h) * 64]);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
                     const V8 kf = widen<DT>(kw[x][c][2 * h], kw[x][c][2 * h + 1], pow2(kb[x]));
 #pragma unroll
-                    for (int b = 0; b < QB; ++b) s[x][b] = Elem<DT>::mfma(kf, qf[b][2 * c + h], s[x][b]);
+                    for (int b = 0; b < QB; ++b) s[x][b] = Elem<DT>::mfma(kf, qv[b], s[x][b]);
                 }
-        }
-        if (more) {
-            load_k(kR);
-            kR = block_row(4 * (t + 2 * step) + (r >> 2));
-        }
+            }
+        __builtin_amdgcn_sched_barrier(0);
+        const u32x4_t vi4 = ve;
+        const int kb1 = 4 * (t + step) + (r >> 2), vb1 = 4 * (t + step) + g;
+        const long vR = block_row(vb1, vp);
+        load_k(block_row(kb1, kp));
+        ve = *reinterpret_cast<const u32x4_t *>(a.vinv + vR);
+        kp = block_page(kb1 + 4 * step);
+        vp = block_page(vb1 + 4 * step);
+        __builtin_amdgcn_sched_barrier(0);
 
         float top[QB];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const float vi = static_cast<float>(byte_of(ve, i));
+            const float vi = static_cast<float>(byte_of(vi4, i));
 #pragma unroll
             for (int b = 0; b < QB; ++b) s[i / 4][b][i % 4] = fmaf(s[i / 4][b][i % 4], cs, bm[b] - vi);
         }
-        if (key0 + ATTEND_TILE > all) {
+        if (uniform(key0 + ATTEND_TILE > all)) {
+            asm volatile("");  // a branch: as selects it would cost every tile 100 instructions
 #pragma unroll
             for (int b = 0; b < QB; ++b)
 #pragma unroll
@@ -273,7 +302,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
         f16x8_t p[2][QB];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const float ib = pow2(byte_of(ve, i));
+            const float ib = pow2(byte_of(vi4, i));
 #pragma unroll
             for (int b = 0; b < QB; ++b) {
                 const float w = exp2_fast(s[i / 4][b][i % 4]);
@@ -289,10 +318,9 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
 #pragma unroll
                 for (int b = 0; b < QB; ++b) o[h][b] = Elem<DT_F16>::mfma(vf, p[x][b], o[h][b]);
             }
-        if (more) {
-            load_v(vR);
-            vR = block_row(4 * (t + 2 * step) + g);
-        }
+        __builtin_amdgcn_sched_barrier(0);
+        load_v(vR);
+        __builtin_amdgcn_sched_barrier(0);
     }
 
     float m[QB];

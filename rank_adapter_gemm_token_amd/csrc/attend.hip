@@ -106,29 +106,6 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
     const bool joined = (it.flags & ATTEND_JOINED) != 0;
     const int step = joined ? ATTEND_WAVES : 1;
 
-    // Queries: lane (r, g) holds row r of each block, elements 64 c + 16 g + 8
-    // h .. + 7, in LDS (16 bytes a lane): in registers they would push the
-    // loop over 256 and its spills would wait for the prefetch.  The wave's
-    // part of LDS is its own until the join.
-    u32x4_t *qf = reinterpret_cast<u32x4_t *>(lds + wave * ROWS * (D + 4)) + lane;
-    int lim[QB];  // keys the row sees
-#pragma unroll
-    for (int b = 0; b < QB; ++b) {
-        const int row = b * 16 + r, i = row / a.gq;
-        const int at = i < it.n_tok ? i : 0;
-        const int head = kvh * a.gq + row - i * a.gq;
-        const uint16_t *q = a.q + toks[at].token * a.q_stride + static_cast<long>(head) * D;
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                qf[(b * 2 * NC + 2 * c + h) * 64] = *reinterpret_cast<const u32x4_t *>(q + c * 64 + g * 16 + h * 8);
-        const int l = it.limit0 + ((it.flags & ATTEND_STEP) ? at : 0);
-        lim[b] = l < it.end ? l : it.end;
-    }
-    // Below this every row sees every key.
-    const int all = it.limit0 < it.end ? it.limit0 : it.end;
-
     // bm = 127 - m: y = c s + (bm - vinv).  thr: what y must pass to move m.
     float bm[QB], thr[QB], l[QB];
     f32x4_t o[NH][QB];
@@ -181,11 +158,44 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
 #pragma unroll
         for (int h = 0; h < NH; ++h) vw[h] = *reinterpret_cast<const u32x4_t *>(p + h * 16 * KV_BLOCK);
     };
+    const int kb0 = 4 * t + (r >> 2), vb0 = 4 * t + g;
     int kp = 0, vp = 0;
     if (t < t_end) {
-        const int kb0 = 4 * t + (r >> 2), vb0 = 4 * t + g;
         kp = block_page(kb0);
         vp = block_page(vb0);
+    }
+
+    // Queries: lane (r, g) holds row r of each block, elements 64 c + 16 g + 8
+    // h .. + 7, in LDS (16 bytes a lane): in registers they would push the
+    // loop over 256 and its spills would wait for the prefetch.  The wave's
+    // part of LDS is its own until the join.  They are asked for before the
+    // first keys, which need as many reads before them (the page; the token).
+    u32x4_t *qf = reinterpret_cast<u32x4_t *>(lds + wave * ROWS * (D + 4)) + lane;
+    u32x4_t q0[QB][2 * NC];
+    int lim[QB];  // keys the row sees
+    int tok[QB], head[QB];
+#pragma unroll
+    for (int b = 0; b < QB; ++b) {
+        const int row = b * 16 + r, i = row / a.gq;
+        const int at = i < it.n_tok ? i : 0;
+        head[b] = kvh * a.gq + row - i * a.gq;
+        tok[b] = toks[at].token;
+        const int l = it.limit0 + ((it.flags & ATTEND_STEP) ? at : 0);
+        lim[b] = l < it.end ? l : it.end;
+    }
+#pragma unroll
+    for (int b = 0; b < QB; ++b) {
+        const uint16_t *q = a.q + tok[b] * a.q_stride + static_cast<long>(head[b]) * D;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                q0[b][2 * c + h] = *reinterpret_cast<const u32x4_t *>(q + c * 64 + g * 16 + h * 8);
+    }
+    // Below this every row sees every key.
+    const int all = it.limit0 < it.end ? it.limit0 : it.end;
+    __builtin_amdgcn_sched_barrier(0);
+    if (t < t_end) {
         const long vR = block_row(vb0, vp);
         load_k(block_row(kb0, kp));
         ve = *reinterpret_cast<const u32x4_t *>(a.vinv + vR);
@@ -195,6 +205,10 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
         load_v(vR);
         __builtin_amdgcn_sched_barrier(0);
     }
+#pragma unroll
+    for (int b = 0; b < QB; ++b)
+#pragma unroll
+        for (int i = 0; i < 2 * NC; ++i) qf[(b * 2 * NC + i) * 64] = q0[b][i];
 
     for (; t < t_end; t += step) {
         asm volatile("" ::: "memory");  // the queries are read again, not kept

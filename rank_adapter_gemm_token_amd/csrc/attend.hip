@@ -20,6 +20,8 @@
 // for the same rows.  Each wave keeps m, l and O of its own keys; the four
 // waves of a workgroup either work on one item and join at the end, or each
 // on an item of its own.
+#include <type_traits>
+
 #include "attend_plan.hpp"
 #include "dtype.hpp"
 #include "kv_internal.hpp"
@@ -67,12 +69,20 @@ __device__ __forceinline__ float max_over_g(float v) {
     return fmaxf(v, __shfl_xor(v, 32, 64));
 }
 
-constexpr int lds_floats(int D, int QB) { return ATTEND_WAVES * 16 * QB * (D + 4 + 2); }
+// The token (of an item) of a query row: row / gq for row < 64, gq <= 32.
+__device__ __forceinline__ int token_of_row(const AttendArgs &a, int row) { return (row * a.gq_inv) >> 16; }
+
+// LDS: for each wave ATTEND_ROWS rows of D + 4 floats -- its item's queries and
+// tokens, then its O for the join -- and for each of its rows m and l.  The
+// wave's part is at the same place whatever its item's rows: the waves of a
+// workgroup may have items of different sizes.
+constexpr int wave_floats(int D) { return ATTEND_ROWS * (D + 4); }
+constexpr int lds_floats(int D) { return ATTEND_WAVES * (wave_floats(D) + ATTEND_ROWS * 2); }
 
 // Four of a row's elements (d .. d + 3): a partial result, or the output.
 template <int DT, int D>
-__device__ __forceinline__ void emit(const AttendArgs &a, const AttendItem &it, const AttendToken *toks, int i,
-                                     int head, int d, f32x4_t sum, float M, float L) {
+__device__ __forceinline__ void emit(const AttendArgs &a, const AttendItem &it, int token, int i, int head, int d,
+                                     f32x4_t sum, float M, float L) {
     if (it.part0 >= 0) {
         const long at = static_cast<long>(it.part0 + i) * a.heads + head;
         *reinterpret_cast<f32x4_t *>(a.part_o + at * D + d) = sum;
@@ -82,7 +92,7 @@ __device__ __forceinline__ void emit(const AttendArgs &a, const AttendItem &it, 
         }
         return;
     }
-    const long at = static_cast<long>(toks[i].token) * a.heads + head;
+    const long at = static_cast<long>(token) * a.heads + head;
     // No key seen: zeros.  (L is NaN, not 0, where a seen key is poisoned.)
     const float f = L == 0.0f ? 0.0f : 1.0f / L;
     typename Elem<DT>::raw w[4];
@@ -143,7 +153,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
     // are issued one tile ahead, after the scores of the tile before, its
     // values after that tile's second product; the pages of the tile after
     // that are looked up between the two, and first looked at when they are
-    // needed, so that no wait for one of these covers a later one.  Past the last tile they read its last block again.
+    // needed, so that no wait for one of these covers a later one.  Blocks past the end read the last one again.
     u32x4_t kw[4][NC], vw[NH], ke, ve;
     auto load_k = [&](long R) {
         const uint8_t *p = a.k + (R + (r & 3)) * D + g * 16;
@@ -170,13 +180,14 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
     // loop over 256 and its spills would wait for the prefetch.  The wave's
     // part of LDS is its own until the join.  They are asked for before the
     // first keys, which need as many reads before them (the page; the token).
-    u32x4_t *qf = reinterpret_cast<u32x4_t *>(lds + wave * ROWS * (D + 4)) + lane;
+    u32x4_t *qf = reinterpret_cast<u32x4_t *>(lds + wave * wave_floats(D)) + lane;
+    static_assert(QB * 2 * NC * 256 + ROWS <= wave_floats(D), "the queries and tokens fit the wave's part");
     u32x4_t q0[QB][2 * NC];
     int lim[QB];  // keys the row sees
     int tok[QB], head[QB];
 #pragma unroll
     for (int b = 0; b < QB; ++b) {
-        const int row = b * 16 + r, i = row / a.gq;
+        const int row = b * 16 + r, i = token_of_row(a, row);
         const int at = i < it.n_tok ? i : 0;
         head[b] = kvh * a.gq + row - i * a.gq;
         tok[b] = toks[at].token;
@@ -209,8 +220,12 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
     for (int b = 0; b < QB; ++b)
 #pragma unroll
         for (int i = 0; i < 2 * NC; ++i) qf[(b * 2 * NC + i) * 64] = q0[b][i];
+    int *row_token = reinterpret_cast<int *>(qf - lane + QB * 2 * NC * 64) + r;
+    if (g == 0)
+#pragma unroll
+        for (int b = 0; b < QB; ++b) row_token[b * 16] = tok[b];
 
-    for (; t < t_end; t += step) {
+    auto tile = [&](auto more) __attribute__((always_inline)) {
         asm volatile("" ::: "memory");  // the queries are read again, not kept
         const int key0 = t * ATTEND_TILE;
         // Scores.  bf16 holds any element times its scale; fp16 does for
@@ -261,12 +276,15 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
             }
         __builtin_amdgcn_sched_barrier(0);
         const u32x4_t vi4 = ve;
-        const int kb1 = 4 * (t + step) + (r >> 2), vb1 = 4 * (t + step) + g;
-        const long vR = block_row(vb1, vp);
-        load_k(block_row(kb1, kp));
-        ve = *reinterpret_cast<const u32x4_t *>(a.vinv + vR);
-        kp = block_page(kb1 + 4 * step);
-        vp = block_page(vb1 + 4 * step);
+        long vR = 0;
+        if constexpr (more) {
+            const int kb1 = 4 * (t + step) + (r >> 2), vb1 = 4 * (t + step) + g;
+            vR = block_row(vb1, vp);
+            load_k(block_row(kb1, kp));
+            ve = *reinterpret_cast<const u32x4_t *>(a.vinv + vR);
+            kp = block_page(kb1 + 4 * step);
+            vp = block_page(vb1 + 4 * step);
+        }
         __builtin_amdgcn_sched_barrier(0);
 
         float top[QB];
@@ -333,9 +351,11 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
                 for (int b = 0; b < QB; ++b) o[h][b] = Elem<DT_F16>::mfma(vf, p[x][b], o[h][b]);
             }
         __builtin_amdgcn_sched_barrier(0);
-        load_v(vR);
+        if constexpr (more) load_v(vR);
         __builtin_amdgcn_sched_barrier(0);
-    }
+    };
+    for (; t + step < t_end; t += step) tile(std::true_type());
+    if (t < t_end) tile(std::false_type());
 
     float m[QB];
 #pragma unroll
@@ -349,26 +369,26 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
     if (!joined) {
 #pragma unroll
         for (int b = 0; b < QB; ++b) {
-            const int row = b * 16 + r, i = row / a.gq;
+            const int row = b * 16 + r, i = token_of_row(a, row);
             if (i < it.n_tok)
 #pragma unroll
                 for (int h = 0; h < NH; ++h)
-                    emit<DT, D>(a, it, toks, i, kvh * a.gq + row - i * a.gq, h * 16 + g * 4, o[h][b], m[b], l[b]);
+                    emit<DT, D>(a, it, row_token[b * 16], i, kvh * a.gq + row - i * a.gq, h * 16 + g * 4, o[h][b], m[b], l[b]);
         }
         return;
     }
 
     // Join the four waves: O scaled to the workgroup's maximum, added in LDS.
-    float *lo = lds, *lm = lds + ATTEND_WAVES * ROWS * (D + 4);
+    float *lo = lds, *lm = lds + ATTEND_WAVES * wave_floats(D);
 #pragma unroll
     for (int b = 0; b < QB; ++b) {
         if (g == 0) {
-            lm[(wave * ROWS + b * 16 + r) * 2] = m[b];
-            lm[(wave * ROWS + b * 16 + r) * 2 + 1] = l[b];
+            lm[(wave * ATTEND_ROWS + b * 16 + r) * 2] = m[b];
+            lm[(wave * ATTEND_ROWS + b * 16 + r) * 2 + 1] = l[b];
         }
 #pragma unroll
         for (int h = 0; h < NH; ++h)
-            *reinterpret_cast<f32x4_t *>(lo + (wave * ROWS + b * 16 + r) * (D + 4) + h * 16 + g * 4) = o[h][b];
+            *reinterpret_cast<f32x4_t *>(lo + (wave * ATTEND_ROWS + b * 16 + r) * (D + 4) + h * 16 + g * 4) = o[h][b];
     }
     __syncthreads();
     const int n_rows = it.n_tok * a.gq;
@@ -378,7 +398,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
         float mw[ATTEND_WAVES], M = -INFINITY, L = 0.0f;
 #pragma unroll
         for (int w = 0; w < ATTEND_WAVES; ++w) {
-            mw[w] = lm[(w * ROWS + row) * 2];
+            mw[w] = lm[(w * ATTEND_ROWS + row) * 2];
             M = fmaxf(M, mw[w]);
         }
         const float ref = M == -INFINITY ? 0.0f : M;
@@ -386,11 +406,11 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
 #pragma unroll
         for (int w = 0; w < ATTEND_WAVES; ++w) {
             const float f = exp2_fast(mw[w] - ref);
-            L = fmaf(f, lm[(w * ROWS + row) * 2 + 1], L);
-            sum += f * *reinterpret_cast<const f32x4_t *>(lo + (w * ROWS + row) * (D + 4) + d);
+            L = fmaf(f, lm[(w * ATTEND_ROWS + row) * 2 + 1], L);
+            sum += f * *reinterpret_cast<const f32x4_t *>(lo + (w * ATTEND_ROWS + row) * (D + 4) + d);
         }
-        const int i = row / a.gq;
-        emit<DT, D>(a, it, toks, i, kvh * a.gq + row - i * a.gq, d, sum, M, L);
+        const int i = token_of_row(a, row);
+        emit<DT, D>(a, it, toks[i].token, i, kvh * a.gq + row - i * a.gq, d, sum, M, L);
     }
     __syncthreads();  // the next item writes LDS again
 }
@@ -463,7 +483,7 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
 
 template <int DT, int D>
 hipError_t run(const AttendArgs &a, int n_groups, int n_tokens, hipStream_t st) {
-    constexpr size_t lds = lds_floats(D, ATTEND_ROWS / 16) * sizeof(float);
+    constexpr size_t lds = lds_floats(D) * sizeof(float);
     static const hipError_t set = hipFuncSetAttribute(reinterpret_cast<const void *>(k_attend<DT, D>),
                                                       hipFuncAttributeMaxDynamicSharedMemorySize,
                                                       static_cast<int>(lds));

@@ -285,6 +285,7 @@ int lora_attend(lora_kv kv, lora_attend_plan plan, const void *q, int64_t q_stri
     a.heads = plan->n_heads;
     a.kv_heads = plan->n_kv_heads;
     a.gq = plan->n_heads / plan->n_kv_heads;
+    a.gq_inv = (65536 + a.gq - 1) / a.gq;
     a.page_shift = kv->c.page_shift;
     a.n_pages = kv->c.n_pages;
     a.scale = scale * 1.44269504088896340736f;

@@ -49,6 +49,7 @@ struct AttendArgs {
     float *part_o;         // [part rows][heads][dim]
     float *part_ml;        // [part rows][heads][2]
     int heads, kv_heads, gq, page_shift, n_pages;
+    int gq_inv;            // 65536 / gq, rounded up
     float scale;           // softmax scale times log2(e)
 };
 

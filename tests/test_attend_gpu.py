@@ -151,6 +151,19 @@ def test_many_rows_of_one_prefix(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_workgroups_of_items_of_different_sizes(dtype, dim):
+    """So many short sequences that each is one wave's work, with query rows for
+    one and for two blocks side by side in a workgroup."""
+    rng = np.random.default_rng(dim)
+    B = 90
+    q_len = [int(x) for x in rng.integers(1, 9, B)]
+    kv_len = [int(x) for x in rng.integers(8, 200, B)]
+    with Step(q_len, kv_len, [-1] * B, [], 128, 32, dim, 16, dtype) as s:
+        s.check(*s.run(), tokens=set(range(0, sum(q_len), 3)))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
 def test_rows_that_see_nothing(dtype):
     """No keys at all; new tokens before a sequence's first key; an empty
     prefix; sequences with nothing new."""

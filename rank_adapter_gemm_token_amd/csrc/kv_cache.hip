@@ -156,7 +156,7 @@ __global__ __launch_bounds__(256) void k_kv_write(KvCache c, const uint16_t *k, 
             for (int i = 0; i < N / 4; ++i) kw[i] = 0x7F7F7F7Fu, vw[i] = 0u;
         }
         R = row_of(c, slot, head);
-        uint32_t *kd = reinterpret_cast<uint32_t *>(c.k + R * D + l * N);
+        uint32_t *kd = reinterpret_cast<uint32_t *>(c.k + (R & ~15L) * D + key_byte<D>(R & 15, l * N));
 #pragma unroll
         for (int i = 0; i < N / 4; ++i) kd[i] = kw[i];
         if (l == 0) {
@@ -220,7 +220,7 @@ __global__ __launch_bounds__(256) void k_kv_read(KvCache c, const int32_t *slots
     auto keys = [&](int token, long R, bool poison) {
         uint32_t w[N / 4];
 #pragma unroll
-        for (int i = 0; i < N / 4; ++i) w[i] = reinterpret_cast<const uint32_t *>(c.k + R * D + l * N)[i];
+        for (int i = 0; i < N / 4; ++i) w[i] = reinterpret_cast<const uint32_t *>(c.k + (R & ~15L) * D + key_byte<D>(R & 15, l * N))[i];
         put(k, token, w, c.kexp[R], poison);
     };
 

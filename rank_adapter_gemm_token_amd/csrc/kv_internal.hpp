@@ -13,10 +13,13 @@ namespace lora {
 // of e4m3, and an exponent byte b that scales them by 2^(b - 127).  Row
 // (page, head, offset) has the number R = (page * heads + head) * page_size +
 // offset.
-//   keys    element d of row R at byte R * D + d
-//   values  blocks of 16 rows are stored by element: element d of row R at
-//           byte (R - R % 16) * D + d * 16 + R % 16, so that the attention
-//           reads 16 keys' values of one element as one word
+// Blocks of 16 rows (R - R % 16 = B) are stored at byte B * D in the order in
+// which the lanes of an MFMA operand load them, 16 bytes a lane, so that
+// neighbouring lanes read neighbouring bytes:
+//   keys    element d of row B + t at key_byte(t, d) of the block: for every
+//           four rows and 64 elements, 16 elements of the four rows in turn
+//   values  by element: element d of row B + t at d * 16 + t, so that 16 keys'
+//           values of one element are one load
 //   kexp, vinv  exponent bytes, one a row: a key's b, a value's 254 - b, of
 //           which the attention makes 2^-s by a shift
 // Elements are finite, except that a row whose key or value has a value that
@@ -27,6 +30,11 @@ constexpr int KV_BLOCK = 16;        // rows of a block of values
 constexpr int KV_POISON = 0;        // as a float's exponent bits: 0, which no weight of 0 makes NaN
 constexpr int KV_EXP_BIAS = 127;
 constexpr int KV_MIN_EXP = -64;     // least exponent kept: smaller values go to 0
+
+template <int D>
+__host__ __device__ constexpr int key_byte(int t, int d) {
+    return (t / 4) * 4 * D + d / 64 * 256 + d % 64 / 16 * 64 + t % 4 * 16 + d % 16;
+}
 
 struct KvCache {
     uint8_t *k, *v, *kexp, *vinv;

@@ -79,19 +79,32 @@ __device__ __forceinline__ int token_of_row(const AttendArgs &a, int row) { retu
 constexpr int wave_floats(int D) { return ATTEND_ROWS * (D + 4); }
 constexpr int lds_floats(int D) { return ATTEND_WAVES * (wave_floats(D) + ATTEND_ROWS * 2); }
 
-// Four of a row's elements (d .. d + 3): a partial result, or the output.
-template <int DT, int D>
-__device__ __forceinline__ void emit(const AttendArgs &a, const AttendItem &it, int token, int i, int head, int d,
-                                     f32x4_t sum, float M, float L) {
-    if (it.part0 >= 0) {
-        const long at = static_cast<long>(it.part0 + i) * a.heads + head;
-        *reinterpret_cast<f32x4_t *>(a.part_o + at * D + d) = sum;
-        if (d == 0) {
-            a.part_ml[at * 2] = M;
-            a.part_ml[at * 2 + 1] = L;
-        }
+// Partial results are joined either in the launch (HERE), by the workgroup or
+// wave that adds a token's last one, or by a second launch.  HERE they go to
+// the agent's coherence point and come from there: the caches of another XCD
+// may hold a copy that an earlier call left.
+template <bool HERE>
+__device__ __forceinline__ void put8(float *p, float x, float y) {
+    if constexpr (!HERE) {
+        *reinterpret_cast<float2 *>(p) = float2{x, y};
         return;
     }
+    __hip_atomic_store(reinterpret_cast<uint64_t *>(p),
+                       static_cast<uint64_t>(__float_as_uint(y)) << 32 | __float_as_uint(x), __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+}
+
+template <bool HERE>
+__device__ __forceinline__ float2 get8(const float *p) {
+    if constexpr (!HERE) return *reinterpret_cast<const float2 *>(p);
+    const uint64_t w =
+        __hip_atomic_load(reinterpret_cast<const uint64_t *>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return float2{__uint_as_float(static_cast<uint32_t>(w)), __uint_as_float(static_cast<uint32_t>(w >> 32))};
+}
+
+// Four of an output row's elements (d .. d + 3).
+template <int DT, int D>
+__device__ __forceinline__ void put_out(const AttendArgs &a, int token, int head, int d, f32x4_t sum, float M, float L) {
     const long at = static_cast<long>(token) * a.heads + head;
     // No key seen: zeros.  (L is NaN, not 0, where a seen key is poisoned.)
     const float f = L == 0.0f ? 0.0f : 1.0f / L;
@@ -102,9 +115,65 @@ __device__ __forceinline__ void emit(const AttendArgs &a, const AttendItem &it, 
     if (d == 0 && a.lse != nullptr) a.lse[at] = LN2 * (M + log2f(L));
 }
 
+// Four of a row's elements, of token i of the item: a partial result, or the output.
+template <int DT, int D, bool HERE>
+__device__ __forceinline__ void emit(const AttendArgs &a, const AttendItem &it, int token, int i, int head, int d,
+                                     f32x4_t sum, float M, float L) {
+    if (it.part0 < 0) return put_out<DT, D>(a, token, head, d, sum, M, L);
+    const long at = static_cast<long>(it.part0 + i) * a.heads + head;
+    put8<HERE>(a.part_o + at * D + d, sum[0], sum[1]);
+    put8<HERE>(a.part_o + at * D + d + 2, sum[2], sum[3]);
+    if (d == 0) put8<HERE>(a.part_ml + at * 2, M, L);
+}
+
+// Counts this item's partial results of token i (its stores have completed);
+// whether they were the last of the token's for this key/value head.
+__device__ __forceinline__ bool count_parts(const AttendArgs &a, const AttendItem &it, const AttendToken *toks, int i,
+                                            int kvh) {
+    unsigned *cnt = a.count + static_cast<long>(it.tok0 + i) * a.kv_heads + kvh;
+    const unsigned all = static_cast<unsigned>(toks[i].n[0] + toks[i].n[1]);
+    if (__hip_atomic_fetch_add(cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != all - 1) return false;
+    __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return true;
+}
+
+// Joins a token's partial results: four elements of one row.
+template <int DT, int D, bool HERE>
+__device__ __forceinline__ void join_parts(const AttendArgs &a, const AttendToken &tk, int head, int d) {
+    const int n = tk.n[0] + tk.n[1];
+    auto row = [&](int j) {
+        const int p = j < tk.n[0] ? tk.part[0] + j * tk.stride[0] : tk.part[1] + (j - tk.n[0]) * tk.stride[1];
+        return static_cast<long>(p) * a.heads + head;
+    };
+    constexpr int STEP = 4;  // results asked for together
+    float M = -INFINITY, L = 0.0f;
+    f32x4_t sum{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < n; j += STEP) {
+        float2 ml[STEP], lo[STEP], hi[STEP];
+#pragma unroll
+        for (int k = 0; k < STEP; ++k) {
+            const long at = row(j + k < n ? j + k : n - 1);
+            ml[k] = get8<HERE>(a.part_ml + at * 2);
+            lo[k] = get8<HERE>(a.part_o + at * D + d);
+            hi[k] = get8<HERE>(a.part_o + at * D + d + 2);
+        }
+#pragma unroll
+        for (int k = 0; k < STEP; ++k) {
+            if (j + k >= n) break;
+            const float to = fmaxf(M, ml[k].x);
+            const float ref = to == -INFINITY ? 0.0f : to;
+            const float f0 = exp2_fast(M - ref), f1 = exp2_fast(ml[k].x - ref);
+            M = to;
+            L = L * f0 + ml[k].y * f1;
+            sum = sum * f0 + f32x4_t{lo[k].x, lo[k].y, hi[k].x, hi[k].y} * f1;
+        }
+    }
+    put_out<DT, D>(a, tk.token, head, d, sum, M, L);
+}
+
 // One wave's item for one key/value head.  QB blocks of 16 query rows; row =
 // token of the item x query head of the key head.
-template <int DT, int D, int QB>
+template <int DT, int D, int QB, bool HERE>
 __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendItem &it, const AttendToken *toks,
                                             const int32_t *pages, int kvh, int wave, float *lds) {
     using V8 = typename Elem<DT>::vec8;
@@ -380,6 +449,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
         // NaN stays in l even where no finite score has moved m.
         if (l[b] != l[b]) m[b] = l[b];
     }
+    constexpr int PER = D / 4;  // lanes of a row, four elements each
     if (!joined) {
 #pragma unroll
         for (int b = 0; b < QB; ++b) {
@@ -387,7 +457,14 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
             if (i < it.n_tok)
 #pragma unroll
                 for (int h = 0; h < NH; ++h)
-                    emit<DT, D>(a, it, row_token[b * 16], i, kvh * a.gq + row - i * a.gq, h * 16 + g * 4, o[h][b], m[b], l[b]);
+                    emit<DT, D, HERE>(a, it, row_token[b * 16], i, kvh * a.gq + row - i * a.gq, h * 16 + g * 4, o[h][b], m[b], l[b]);
+        }
+        if (!HERE || it.part0 < 0) return;
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        unsigned long long last = __ballot(lane < it.n_tok && count_parts(a, it, toks, lane, kvh));
+        for (; last != 0; last &= last - 1) {
+            const AttendToken tk = toks[__builtin_ctzll(last)];
+            for (int at = lane; at < a.gq * PER; at += 64) join_parts<DT, D, HERE>(a, tk, kvh * a.gq + at / PER, at % PER * 4);
         }
         return;
     }
@@ -406,7 +483,6 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
     }
     __syncthreads();
     const int n_rows = it.n_tok * a.gq;
-    constexpr int PER = D / 4;  // lanes of a row, four elements each
     for (int at = threadIdx.x; at < n_rows * PER; at += 256) {
         const int row = at / PER, d = at % PER * 4;
         float mw[ATTEND_WAVES], M = -INFINITY, L = 0.0f;
@@ -424,7 +500,23 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
             sum += f * *reinterpret_cast<const f32x4_t *>(lo + (w * ATTEND_ROWS + row) * (D + 4) + d);
         }
         const int i = token_of_row(a, row);
-        emit<DT, D>(a, it, toks[i].token, i, kvh * a.gq + row - i * a.gq, d, sum, M, L);
+        emit<DT, D, HERE>(a, it, toks[i].token, i, kvh * a.gq + row - i * a.gq, d, sum, M, L);
+    }
+    if (HERE && it.part0 >= 0) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        unsigned long long *last = reinterpret_cast<unsigned long long *>(lm);
+        if (wave == 0) {
+            const unsigned long long mine = __ballot(lane < it.n_tok && count_parts(a, it, toks, lane, kvh));
+            if (lane == 0) *last = mine;
+        }
+        __syncthreads();
+        unsigned long long todo = *last;
+        for (; todo != 0; todo &= todo - 1) {
+            const AttendToken tk = toks[__builtin_ctzll(todo)];
+            for (int at = threadIdx.x; at < a.gq * PER; at += 256)
+                join_parts<DT, D, HERE>(a, tk, kvh * a.gq + at / PER, at % PER * 4);
+        }
     }
     __syncthreads();  // the next item writes LDS again
 }
@@ -436,7 +528,7 @@ __device__ __forceinline__ bool plan_fits(const AttendArgs &a, const AttendHeade
     return h->page_size == 1 << a.page_shift && h->n_pages == a.n_pages;
 }
 
-template <int DT, int D>
+template <int DT, int D, bool HERE>
 __global__ __launch_bounds__(256, 2) void k_attend(AttendArgs a) {
     extern __shared__ float lds[];
     const AttendHeader *h = reinterpret_cast<const AttendHeader *>(a.meta);
@@ -445,19 +537,17 @@ __global__ __launch_bounds__(256, 2) void k_attend(AttendArgs a) {
     const int32_t *pages = reinterpret_cast<const int32_t *>(a.meta + h->page_off);
     const int n = plan_fits(a, h) ? h->n_groups * a.kv_heads : 0;
     const int wave = uniform(threadIdx.x >> 6);
-    // The grid has a workgroup for each of the plan's at launch; a graph
-    // replayed after a new plan may find more.
     for (int w = blockIdx.x; w < n; w += gridDim.x) {
         const int i = w / a.kv_heads, kvh = w - i * a.kv_heads;
         const AttendItem it = items[i * ATTEND_WAVES + wave];
         if (it.n_tok * a.gq > 16)
-            attend_item<DT, D, 2>(a, it, toks + it.tok0, pages + it.page0, kvh, wave, lds);
+            attend_item<DT, D, 2, HERE>(a, it, toks + it.tok0, pages + it.page0, kvh, wave, lds);
         else if (it.n_tok > 0)
-            attend_item<DT, D, 1>(a, it, toks + it.tok0, pages + it.page0, kvh, wave, lds);
+            attend_item<DT, D, 1, HERE>(a, it, toks + it.tok0, pages + it.page0, kvh, wave, lds);
     }
 }
 
-// Join the partial results of each (token, head): D / 4 lanes a row.
+// The second launch: D / 4 lanes join a row.
 template <int DT, int D>
 __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
     const AttendHeader *h = reinterpret_cast<const AttendHeader *>(a.meta);
@@ -468,48 +558,41 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
          row += static_cast<long>(gridDim.x) * ROWS) {
         const int s = static_cast<int>(row / a.heads), head = static_cast<int>(row - static_cast<long>(s) * a.heads);
         const AttendToken tk = toks[s];
-        const int parts = tk.n[0] + tk.n[1];
-        if (parts == 0) continue;
-        const int d = threadIdx.x % PER * 4;
-        float M = -INFINITY, L = 0.0f;
-        f32x4_t sum{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int k = 0; k < 2; ++k)
-            for (int j = 0; j < tk.n[k]; ++j) {
-                const long at = static_cast<long>(tk.part[k] + j * tk.stride[k]) * a.heads + head;
-                const float pm = a.part_ml[at * 2], pl = a.part_ml[at * 2 + 1];
-                const f32x4_t po = *reinterpret_cast<const f32x4_t *>(a.part_o + at * D + d);
-                const float to = fmaxf(M, pm);
-                const float ref = to == -INFINITY ? 0.0f : to;
-                const float f0 = exp2_fast(M - ref), f1 = exp2_fast(pm - ref);
-                M = to;
-                L = L * f0 + pl * f1;
-                sum = sum * f0 + po * f1;
-            }
-        const long at_out = static_cast<long>(tk.token) * a.heads + head;
-        const float f = L == 0.0f ? 0.0f : 1.0f / L;
-        typename Elem<DT>::raw w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = Elem<DT>::from_f(sum[j] * f);
-        *reinterpret_cast<uint2 *>(a.out + at_out * D + d) = *reinterpret_cast<const uint2 *>(w);
-        if (d == 0 && a.lse != nullptr) a.lse[at_out] = LN2 * (M + log2f(L));
+        if (tk.n[0] + tk.n[1] > 0) join_parts<DT, D, false>(a, tk, head, threadIdx.x % PER * 4);
     }
 }
 
-template <int DT, int D>
+// Grids are as large as the plan at launch asks for; a graph replayed after a
+// new plan may find more, or partial results where there were none.
+template <int DT, int D, bool HERE>
 hipError_t run(const AttendArgs &a, int n_groups, int n_tokens, hipStream_t st) {
     constexpr size_t lds = lds_floats(D) * sizeof(float);
-    static const hipError_t set = hipFuncSetAttribute(reinterpret_cast<const void *>(k_attend<DT, D>),
+    static const hipError_t set = hipFuncSetAttribute(reinterpret_cast<const void *>(k_attend<DT, D, HERE>),
                                                       hipFuncAttributeMaxDynamicSharedMemorySize,
                                                       static_cast<int>(lds));
     if (set != hipSuccess) return set;
-    const long wgs = static_cast<long>(n_groups) * a.kv_heads;
-    k_attend<DT, D><<<static_cast<unsigned>(wgs < 1 ? 1 : wgs > 65536 ? 65536 : wgs), 256, lds, st>>>(a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const long rows = static_cast<long>(n_tokens) * a.heads, per = 256 / (D / 4);
-    const long joins = (rows + per - 1) / per;
-    k_attend_join<DT, D><<<static_cast<unsigned>(joins < 1 ? 1 : joins > 65536 ? 65536 : joins), 256, 0, st>>>(a);
+    auto grid = [](long n) { return static_cast<unsigned>(n < 1 ? 1 : n > 65536 ? 65536 : n); };
+    k_attend<DT, D, HERE><<<grid(static_cast<long>(n_groups) * a.kv_heads), 256, lds, st>>>(a);
+    if constexpr (!HERE) {
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        const long rows = static_cast<long>(n_tokens) * a.heads, per = 256 / (D / 4);
+        k_attend_join<DT, D><<<grid((rows + per - 1) / per), 256, 0, st>>>(a);
+    }
     return hipGetLastError();
+}
+
+// Joining in the launch saves the second one (5 us, 16 partial results of one
+// sequence: 10.0 us instead of 12.5), but each wave then waits for its stores
+// and its count before it ends (4 us); where workgroups follow one another on
+// a CU that is paid several times (64 decoding sequences: 49 us instead of
+// 43).  So: where all of them run at once, two a CU.
+constexpr int JOIN_HERE_WGS = 512;
+
+template <int DT, int D>
+hipError_t run(const AttendArgs &a, int n_groups, int n_tokens, hipStream_t st) {
+    return static_cast<long>(n_groups) * a.kv_heads <= JOIN_HERE_WGS ? run<DT, D, true>(a, n_groups, n_tokens, st)
+                                                                     : run<DT, D, false>(a, n_groups, n_tokens, st);
 }
 
 }  // namespace

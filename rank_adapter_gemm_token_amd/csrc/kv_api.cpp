@@ -33,6 +33,7 @@ struct lora_attend_plan_s {
     lora::AttendPlanner planner;
     char *mem = nullptr;                    // the plan as the kernels read it, then the partial results
     float *part_o = nullptr, *part_ml = nullptr;
+    unsigned *count = nullptr;
     // Two pinned copies of the plan: one may still be on its way to the device
     // while the next is written.
     void *host[2] = {nullptr, nullptr};
@@ -193,8 +194,14 @@ int lora_attend_plan_create(int max_seqs, int max_groups, int max_tokens, int ma
     const size_t plan_bytes = align_up(p->planner.max_bytes(), 256);
     const size_t rows = static_cast<size_t>(p->planner.max_part_rows()) * n_heads;
     const size_t o_bytes = align_up(rows * head_dim * 4, 256);
+    const size_t ml_bytes = align_up(rows * 8, 256);
+    const size_t cnt_bytes = static_cast<size_t>(max_tokens) * n_kv_heads * 4;
     hipError_t e = hipGetDevice(&p->device);
-    if (e == hipSuccess) e = hipMalloc(reinterpret_cast<void **>(&p->mem), plan_bytes + o_bytes + rows * 8);
+    if (e == hipSuccess)
+        e = hipMalloc(reinterpret_cast<void **>(&p->mem), plan_bytes + o_bytes + ml_bytes + cnt_bytes);
+    // The counters start at 0; every call leaves them there.
+    if (e == hipSuccess) e = hipMemset(p->mem + plan_bytes + o_bytes + ml_bytes, 0, cnt_bytes);
+    if (e == hipSuccess) e = hipDeviceSynchronize();
     for (int i = 0; i < 2; ++i) {
         if (e == hipSuccess) e = hipHostMalloc(&p->host[i], plan_bytes, hipHostMallocDefault);
         if (e == hipSuccess) e = hipEventCreateWithFlags(&p->sent[i], hipEventDisableTiming);
@@ -207,6 +214,7 @@ int lora_attend_plan_create(int max_seqs, int max_groups, int max_tokens, int ma
     }
     p->part_o = reinterpret_cast<float *>(p->mem + plan_bytes);
     p->part_ml = reinterpret_cast<float *>(p->mem + plan_bytes + o_bytes);
+    p->count = reinterpret_cast<unsigned *>(p->mem + plan_bytes + o_bytes + ml_bytes);
     *out = p;
     return LORA_OK;
 }
@@ -282,6 +290,7 @@ int lora_attend(lora_kv kv, lora_attend_plan plan, const void *q, int64_t q_stri
     a.lse = lse;
     a.part_o = plan->part_o;
     a.part_ml = plan->part_ml;
+    a.count = plan->count;
     a.heads = plan->n_heads;
     a.kv_heads = plan->n_kv_heads;
     a.gq = plan->n_heads / plan->n_kv_heads;

@@ -56,6 +56,7 @@ struct AttendArgs {
     float *lse;            // [tokens][heads] or null
     float *part_o;         // [part rows][heads][dim]
     float *part_ml;        // [part rows][heads][2]
+    unsigned *count;       // [tokens][kv_heads] partial results so far; 0 between calls
     int heads, kv_heads, gq, page_shift, n_pages;
     int gq_inv;            // 65536 / gq, rounded up
     float scale;           // softmax scale times log2(e)

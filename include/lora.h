@@ -92,7 +92,7 @@ typedef enum { LORA_MODE_AUTO = 0, LORA_MODE_FUSED = 1, LORA_MODE_SEPARATE = 2 }
 #define LORA_ATTEND_MAX_TOKENS 65536   /* sequences, groups and new tokens of a plan */
 #define LORA_ATTEND_MAX_PAGES (1 << 26) /* pages a plan's sequences and prefixes hold together */
 #define LORA_VERIFY_MAX_SEQS 65535     /* sequences of a verifier */
-#define LORA_VERIFY_MAX_VOCAB (1 << 24)
+#define LORA_VERIFY_MAX_VOCAB (1 << 21)
 #define LORA_VERIFY_MAX_DRAFTS 63      /* drafted tokens of one sequence */
 
 /* Status codes. */

@@ -20,6 +20,9 @@ using lora::aligned;
 using lora::DeviceGuard;
 using lora::hip_fail;
 
+static_assert(LORA_VERIFY_MAX_VOCAB == lora::VERIFY_PART * lora::VERIFY_PARTS, "a lane for each part of a row");
+static_assert(LORA_VERIFY_MAX_DRAFTS == lora::VERIFY_MAX_DRAFTS, "a lane for each drafted token");
+
 struct lora_kv_s {
     int device = 0;
     int page_size = 0;
@@ -366,13 +369,9 @@ int lora_verify(lora_verifier v, const void *p_target, const void *p_draft, lora
     a.n_seqs = n_seqs;
     a.n_rows = n_rows;
     a.vocab = vocab;
-    // Parts of one step, of more where that makes over VERIFY_PARTS of them;
-    // as many parts a workgroup as leaves about eight workgroups a CU (2048):
-    // each has the same few dependent reads before its first part.
-    const int steps = (vocab + lora::VERIFY_STEP - 1) / lora::VERIFY_STEP;
-    a.part = lora::VERIFY_STEP * ((steps + lora::VERIFY_PARTS - 1) / lora::VERIFY_PARTS);
-    a.parts = (vocab + a.part - 1) / a.part;
-    const int wgs = 2048 / n_seqs;  // of a sequence
+    // A workgroup fills a CU: as many to a sequence as there are CUs for it.
+    a.parts = (vocab + lora::VERIFY_PART - 1) / lora::VERIFY_PART;
+    const int wgs = 256 / n_seqs;
     a.group = wgs < 1 ? a.parts : (a.parts + wgs - 1) / wgs;
     HIP_TRY(lora::launch_verify(a, static_cast<int>(dtype), static_cast<hipStream_t>(stream)));
     return LORA_OK;

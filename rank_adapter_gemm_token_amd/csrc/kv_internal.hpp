@@ -72,10 +72,10 @@ struct VerifyArgs {
     double *sums;          // [seqs][VERIFY_PARTS]
     unsigned *count;       // [seqs], 0 between calls
     int n_seqs, n_rows, vocab;
-    int part, parts, group;  // elements of a part, parts of a row, parts of a workgroup
+    int parts, group;      // parts of a row, parts of a workgroup
 };
+constexpr int VERIFY_PART = 32768;    // elements of a part of a row
 constexpr int VERIFY_PARTS = 64;      // parts of a row at most
-constexpr int VERIFY_STEP = 2048;     // elements a workgroup takes at a time
 constexpr int VERIFY_MAX_DRAFTS = 63; // drafted tokens of a sequence
 
 hipError_t launch_verify(const VerifyArgs &a, int dtype, hipStream_t st);

@@ -16,24 +16,17 @@ namespace lora {
 
 namespace {
 
-constexpr int THREADS = 256;
-constexpr int STEP = 8;  // elements a thread takes at a time
-constexpr int NONE = 0x7FFFFFFF;
+constexpr int THREADS = 1024;
+constexpr int WAVES = THREADS / 64;
+constexpr int STEP = 8;    // neighbouring elements of a thread
+constexpr int ROUNDS = 4;  // of these, asked for together
+constexpr int SEGS = ROUNDS * WAVES;  // runs of 64 * STEP elements in a part
+static_assert(THREADS * STEP * ROUNDS == VERIFY_PART && SEGS == 64, "a lane for each segment of a part");
 
 template <int DT>
 struct Wide {
     typename Elem<DT>::raw w[STEP];
 };
-
-// Eight neighbouring probabilities; rows start at any element, so the load is
-// as wide as the hardware makes of an unaligned one.
-template <int DT>
-__device__ __forceinline__ void load_p(const typename Elem<DT>::raw *p, float (&x)[STEP]) {
-    Wide<DT> t;
-    __builtin_memcpy(&t, p, sizeof t);
-#pragma unroll
-    for (int i = 0; i < STEP; ++i) x[i] = Elem<DT>::to_f(t.w[i]);
-}
 
 // A weight: what is not above zero (NaN among it) counts as nothing.
 __device__ __forceinline__ double weight(float p, float q) {
@@ -47,63 +40,75 @@ __device__ __forceinline__ double wave_sum(double v) {
     return v;
 }
 
-// Sum over the workgroup's threads, to all of them.
-__device__ __forceinline__ double block_sum(double v, double *s) {
-    v = wave_sum(v);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
-    __syncthreads();
-    return (s[0] + s[1]) + (s[2] + s[3]);
-}
-
-// Inclusive running sum over the workgroup's threads.
-__device__ __forceinline__ double block_scan(double v, double *s) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// Inclusive running sum over the wave's lanes.
+__device__ __forceinline__ double wave_scan(double v) {
+    const int lane = threadIdx.x & 63;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const double o = __shfl_up(v, d, 64);
-        if (lane >= d) v += o;
+    for (int k = 1; k < 64; k <<= 1) {
+        const double o = __shfl_up(v, k, 64);
+        if (lane >= k) v += o;
     }
-    __syncthreads();
-    if (lane == 63) s[wave] = v;
-    __syncthreads();
-    for (int w = 0; w < wave; ++w) v += s[w];
     return v;
 }
 
-// The sum of eight neighbouring weights, index i .. i + 7, those below hi.
+// Of lanes that hold neighbouring runs' sums v, running r: the first whose
+// running sum passes `aim`, or else the last with any weight.
+__device__ __forceinline__ int pick_lane(double v, double r, double aim) {
+    const unsigned long long passes = __ballot(r > aim), some = __ballot(v > 0.0);
+    return uniform(passes ? __builtin_ctzll(passes) : some ? 63 - __builtin_clzll(some) : 0);
+}
+
+// The weights of one part of a row, in the workgroup's registers: thread t has
+// elements (round * 1024 + t) * 8 .. + 7 of the part.
 template <int DT>
-__device__ __forceinline__ double weights(const typename Elem<DT>::raw *p, const typename Elem<DT>::raw *q, int i,
-                                          int hi) {
-    float x[STEP] = {}, y[STEP] = {};
-    if (i + STEP <= hi) {
-        load_p<DT>(p + i, x);
-        if (q != nullptr) load_p<DT>(q + i, y);
-    } else {
-#pragma unroll
-        for (int j = 0; j < STEP; ++j)
-            if (i + j < hi) {
-                x[j] = Elem<DT>::to_f(p[i + j]);
-                if (q != nullptr) y[j] = Elem<DT>::to_f(q[i + j]);
-            }
-    }
-    double v = 0.0;
-#pragma unroll
-    for (int j = 0; j < STEP; ++j) v += weight(x[j], y[j]);
-    return v;
-}
+struct Part {
+    Wide<DT> p[ROUNDS], q[ROUNDS];
 
-// The row that a sequence's new token is drawn from is cut into up to
-// VERIFY_PARTS parts.  Workgroup (c, b) finds that row of sequence b itself (a
-// handful of reads), adds up `group` of its parts, and the last of a
-// sequence's workgroups to finish picks the part, reads it once more and picks
-// the token.
+    __device__ __forceinline__ void load(const typename Elem<DT>::raw *pr, const typename Elem<DT>::raw *qr, int part,
+                                         int V) {
+#pragma unroll
+        for (int k = 0; k < ROUNDS; ++k) {
+            const int i = part * VERIFY_PART + (k * THREADS + static_cast<int>(threadIdx.x)) * STEP;
+            p[k] = q[k] = Wide<DT>{};
+            // Rows start at any element, so the load is as wide as the
+            // hardware makes of an unaligned one.
+            if (i + STEP <= V) {
+                __builtin_memcpy(&p[k], pr + i, sizeof p[k]);
+                if (qr != nullptr) __builtin_memcpy(&q[k], qr + i, sizeof q[k]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < STEP; ++j)
+                    if (i + j < V) {
+                        p[k].w[j] = pr[i + j];
+                        if (qr != nullptr) q[k].w[j] = qr[i + j];
+                    }
+            }
+        }
+    }
+    __device__ __forceinline__ double at(int k, int j) const {
+        return weight(Elem<DT>::to_f(p[k].w[j]), Elem<DT>::to_f(q[k].w[j]));
+    }
+    __device__ __forceinline__ double sum(int k) const {
+        double v = 0.0;
+#pragma unroll
+        for (int j = 0; j < STEP; ++j) v += at(k, j);
+        return v;
+    }
+};
+
+// Workgroup (c, b) finds the row that sequence b's new token is drawn from (a
+// handful of reads), adds up `group` of the row's parts, and the last of a
+// sequence's workgroups to finish picks the part, in it the segment, the lane
+// and the token.  A part's 32768 elements are in flight at once in one
+// workgroup: a row of that much needs no second workgroup and no second read
+// (64 sequences, 32000 entries, fp32: 8 us; with 16 workgroups a sequence that
+// count each other 18.6 us).
 template <int DT>
 __global__ __launch_bounds__(THREADS) void k_verify(VerifyArgs a) {
     using raw = typename Elem<DT>::raw;
     const raw *p = static_cast<const raw *>(a.p), *q = static_cast<const raw *>(a.q);
     const int b = blockIdx.y, c = blockIdx.x, t = threadIdx.x, V = a.vocab;
-    __shared__ double s[VERIFY_PARTS][THREADS / 64];
+    __shared__ double seg[SEGS];
     __shared__ int found;
     __shared__ unsigned arrived;
 
@@ -116,16 +121,17 @@ __global__ __launch_bounds__(THREADS) void k_verify(VerifyArgs a) {
         return;
     }
     // Lane i looks at drafted token i.
-    const int lane = t & 63, wave = t >> 6;
+    const int lane = t & 63, wave = uniform(t >> 6);
     bool keep = false, bad = false;
     int d = -1;
+    const float u = lane <= n ? a.u[r0 + lane] : 0.0f;
     if (lane < n) {
         d = a.draft[r0 - b + lane];
         bad = d < 0 || d >= V;
         if (!bad) {
             const double pv = Elem<DT>::to_f(p[static_cast<long>(r0 + lane) * V + d]);
             const double qv = Elem<DT>::to_f(q[static_cast<long>(r0 - b + lane) * V + d]);
-            keep = static_cast<double>(a.u[r0 + lane]) * qv < pv;
+            keep = static_cast<double>(u) * qv < pv;
         }
     }
     const bool any_bad = __ballot(bad) != 0;
@@ -140,102 +146,87 @@ __global__ __launch_bounds__(THREADS) void k_verify(VerifyArgs a) {
     }
     const raw *pr = p + static_cast<long>(r0 + kept) * V;
     const raw *qr = kept < n ? q + static_cast<long>(r0 - b + kept) * V : nullptr;
+    const double u_new = static_cast<double>(__shfl(u, kept, 64));
 
-    const int p0 = c * a.group, p1 = p0 + a.group < a.parts ? p0 + a.group : a.parts;
-#pragma unroll 2
-    for (int part = p0; part < p1; ++part) {
-        const int lo = part * a.part, hi = lo + a.part < V ? lo + a.part : V;
-        double v = 0.0;
-        for (int i = lo + t * STEP; i < hi; i += THREADS * STEP) v += weights<DT>(pr, qr, i, hi);
-        v = wave_sum(v);
-        if (lane == 0) s[part - p0][wave] = v;
-    }
-    __syncthreads();
-    double *sums = a.sums + static_cast<long>(b) * VERIFY_PARTS;
-    if (wave == 0) {
-        if (lane < p1 - p0)
-            __hip_atomic_store(sums + p0 + lane, (s[lane][0] + s[lane][1]) + (s[lane][2] + s[lane][3]),
-                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        // The sums are at the agent's coherence point before the workgroup is
-        // counted (a release at agent scope would write the whole L2 back:
-        // 480 us instead of 40 for 256 sequences).
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        if (lane == 0) {
-            arrived = __hip_atomic_fetch_add(a.count + b, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            found = NONE;
-        }
-    }
-    __syncthreads();
-    if (arrived != gridDim.x - 1) return;
-    if (t == 0) __hip_atomic_store(a.count + b, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-
-    // Lane i holds part i's sum (VERIFY_PARTS is a wave's width).
+    // Lane i of part_sum: the sum of part i.
+    Part<DT> held;
     double part_sum = 0.0;
-    if (lane < a.parts) part_sum = __hip_atomic_load(sums + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    double run = part_sum;
+    auto add_parts = [&](int p0, int p1) {
+        for (int part = p0; part < p1; ++part) {
+            held.load(pr, qr, part, V);
+            __syncthreads();  // the segments of the part before have been read
 #pragma unroll
-    for (int k = 1; k < 64; k <<= 1) {
-        const double o = __shfl_up(run, k, 64);
-        if (lane >= k) run += o;
+            for (int k = 0; k < ROUNDS; ++k) {
+                const double v = wave_sum(held.sum(k));
+                if (lane == 0) seg[k * WAVES + wave] = v;
+            }
+            __syncthreads();
+            const double all = wave_sum(seg[lane]);
+            if (lane == part) part_sum = all;
+        }
+    };
+    const int p0 = c * a.group, p1 = p0 + a.group < a.parts ? p0 + a.group : a.parts;
+    add_parts(p0, p1);
+    int at = p1 - 1;  // the part in `held`
+    if (gridDim.x > 1) {
+        double *sums = a.sums + static_cast<long>(b) * VERIFY_PARTS;
+        if (wave == 0) {
+            if (lane >= p0 && lane < p1)
+                __hip_atomic_store(sums + lane, part_sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            // The sums are at the agent's coherence point before the workgroup
+            // is counted (a release at agent scope would write the whole L2
+            // back: 480 us instead of 40 for 256 sequences of 64 workgroups).
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            if (lane == 0)
+                arrived = __hip_atomic_fetch_add(a.count + b, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        __syncthreads();
+        if (arrived != gridDim.x - 1) return;
+        if (t == 0) __hip_atomic_store(a.count + b, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (lane < a.parts) part_sum = __hip_atomic_load(sums + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    double total = __shfl(run, 63, 64);
-    // The part to look in, and the running sum before it.
-    int from = 0, to = V;
-    double base = 0.0;
-    if (!(total > 0.0) && qr != nullptr) {
+    if (!(wave_sum(part_sum) > 0.0) && qr != nullptr) {
         // Nothing of the difference is left: the target's row, as a whole.
         qr = nullptr;
-        double v = 0.0;
-        for (int i = t * STEP; i < V; i += THREADS * STEP) v += weights<DT>(pr, qr, i, V);
-        total = block_sum(v, s[0]);
-    } else {
-        const double aim = static_cast<double>(a.u[r0 + kept]) * total;
-        // The first part whose running sum passes, or the last with any weight.
-        const unsigned long long passes = __ballot(run > aim), some = __ballot(part_sum > 0.0);
-        const int pick = uniform(passes ? __builtin_ctzll(passes) : some ? 63 - __builtin_clzll(some) : 0);
-        if (pick > 0) base = __shfl(run, pick - 1, 64);
-        from = pick * a.part;
-        to = from + a.part < V ? from + a.part : V;
+        part_sum = 0.0;
+        add_parts(0, a.parts);
+        at = a.parts - 1;
     }
+    double run = wave_scan(part_sum);
+    const double total = __shfl(run, 63, 64), aim = u_new * total;
     int token = -1;
     if (total > 0.0 && total <= 1.7976931348623157e308) {
-        const double aim = static_cast<double>(a.u[r0 + kept]) * total;
-        int last = -1;  // the last index with any weight, if none passes
-        for (int at = from; at < to; at += THREADS * STEP) {
-            double w[STEP], mine = 0.0;
-            const int i = at + t * STEP;
+        const int part = pick_lane(part_sum, run, aim);
+        double base = part > 0 ? __shfl(run, part - 1, 64) : 0.0;
+        if (part != at) add_parts(part, part + 1);
+        // The segment, by every wave; the rest by the wave that has it.
+        const double v = seg[lane];
+        run = base + wave_scan(v);
+        const int s = pick_lane(v, run, aim);
+        if (s > 0) base = __shfl(run, s - 1, 64);
+        if (wave == s % WAVES) {
 #pragma unroll
-            for (int j = 0; j < STEP; ++j) {
-                w[j] = i + j < to ? weight(Elem<DT>::to_f(pr[i + j]), qr != nullptr ? Elem<DT>::to_f(qr[i + j]) : 0.0f)
-                                  : 0.0;
-                mine += w[j];
-            }
-            const double incl = block_scan(mine, s[0]);
-            double r = base + (incl - mine);
-            int hit = NONE;
+            for (int k = 0; k < ROUNDS; ++k) {
+                if (k != s / WAVES) continue;
+                const double mine = held.sum(k), upto = base + wave_scan(mine);
+                const int l = pick_lane(mine, upto, aim);
+                if (l > 0) base = __shfl(upto, l - 1, 64);
+                if (lane == l) {
+                    const int i = part * VERIFY_PART + (k * THREADS + t) * STEP;
+                    int hit = -1, last = -1;
 #pragma unroll
-            for (int j = 0; j < STEP; ++j) {
-                r += w[j];
-                if (w[j] > 0.0) last = i + j;
-                if (hit == NONE && w[j] > 0.0 && r > aim) hit = i + j;
+                    for (int j = 0; j < STEP; ++j) {
+                        const double w = held.at(k, j);
+                        base += w;
+                        if (w > 0.0) last = i + j;
+                        if (hit < 0 && w > 0.0 && base > aim) hit = i + j;
+                    }
+                    found = hit >= 0 ? hit : last;  // last: rounding kept the sum at or below the aim
+                }
             }
-            if (hit != NONE) atomicMin(&found, hit);
-            __syncthreads();
-            if (found != NONE) break;
-            if (t == THREADS - 1) s[0][0] = base + incl;
-            __syncthreads();
-            base = s[0][0];
         }
+        __syncthreads();
         token = found;
-        if (token == NONE) {
-            // Rounding kept the running sum at or below the aim.
-            __syncthreads();
-            if (t == 0) found = -1;
-            __syncthreads();
-            atomicMax(&found, last);
-            __syncthreads();
-            token = found;
-        }
     }
     // Nothing to draw from (no weight, or not finite): no answer for the sequence.
     if (t == 0) a.accepted[b] = token >= 0 ? kept : -1;

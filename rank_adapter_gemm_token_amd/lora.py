@@ -28,7 +28,7 @@ LORA_KV_MAX_PAGE = 1024
 LORA_ATTEND_MAX_TOKENS = 65536
 LORA_ATTEND_MAX_PAGES = 1 << 26
 LORA_VERIFY_MAX_SEQS = 65535
-LORA_VERIFY_MAX_VOCAB = 1 << 24
+LORA_VERIFY_MAX_VOCAB = 1 << 21
 LORA_VERIFY_MAX_DRAFTS = 63
 
 LORA_OK = 0
@@ -181,7 +181,8 @@ def _ptr(t):
 
 def _stream(s):
     if s is None:
-        return torch.cuda.current_stream().cuda_stream
+        # torch.cuda.current_stream() builds a Stream object: 2.8 us a call instead of 0.2.
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(s, int):
         return s
     return s.cuda_stream

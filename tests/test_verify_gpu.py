@@ -65,6 +65,26 @@ def test_longest_drafts_and_one_sequence():
     same(*batch([1] * 300, 333, "f32", 4))
 
 
+@pytest.mark.parametrize("V", [32767, 32768, 32769, 65536, 99999, 1 << 21])
+@pytest.mark.parametrize("B", [1, 40, 300])
+def test_rows_of_several_parts(V, B):
+    """Rows of one and of many parts, by one workgroup and by several; few
+    probabilities that are not 0, so that whole parts have none."""
+    if B * V > 1 << 23:
+        B = max(1, (1 << 23) // V)
+    g = torch.Generator().manual_seed(V + B)
+    n = [i % 2 for i in range(B)]
+    row0 = [0] + [int(x) for x in np.cumsum(np.array(n) + 1)]
+    p, q = torch.zeros(row0[-1], V), torch.zeros(sum(n), V)
+    for x in (p, q):
+        at = torch.randint(0, V, (len(x), 5), generator=g)
+        x.scatter_(1, at, torch.rand(at.shape, generator=g))
+    draft = [int(x) for x in q.argmax(1)]
+    u = torch.rand(row0[-1], generator=g).tolist()
+    u[0] = 1 - 2.0 ** -24
+    same(p.cuda(), q.cuda(), draft, row0, u)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 def test_borders(dtype):
     """u at both ends; p and q equal, far apart, with zeros; ties of the
@@ -158,7 +178,7 @@ def test_refusals():
     good = [v, p.data_ptr(), q.data_ptr(), 0, 64, d.data_ptr(), r.data_ptr(), x.data_ptr(), 2, 4, t.data_ptr(),
             a.data_ptr(), None]
     assert lib.lora_verify(*good) == lora.LORA_OK
-    for at, bad in [(1, None), (2, None), (3, 5), (4, 0), (4, (1 << 24) + 1), (5, None), (6, None), (7, None), (8, -1),
+    for at, bad in [(1, None), (2, None), (3, 5), (4, 0), (4, (1 << 21) + 1), (5, None), (6, None), (7, None), (8, -1),
                     (9, -1), (10, None), (11, None), (1, p.data_ptr() + 2), (6, r.data_ptr() + 1)]:
         args = list(good)
         args[at] = bad

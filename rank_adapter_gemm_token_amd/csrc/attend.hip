@@ -3,15 +3,15 @@
 // its query rows.
 //
 // In the log2 domain, for one query row over keys t with scores s_t, value
-// exponents b_t (v_t = 2^b_t v8_t) and c = scale * log2(e), against a whole
-// number m near max(c s_t + b_t):
+// exponents b_t (v_t = 2^b_t v8_t) and c = scale * log2(e), against an m near
+// max(c s_t + b_t):
 //     y_t = c s_t + (b_t - m),   p_t = 2^y_t
 //     O = sum p_t v8_t,    l = sum p_t 2^-b_t,   out = O / l,
 //     lse = ln 2 * (m + log2 l).
 // The value's exponent goes into the weight, so that the values' elements
 // feed the matrix instruction as they are and p_t is near or below 1 for
-// values of any size: exact enough in fp16.  b_t - m is exact, so y_t is
-// rounded once, where it is small.
+// values of any size: exact enough in fp16.  m has at most 15 bits after the
+// point, so b_t - m is exact and y_t is rounded once, where it is small.
 //
 // Both products are computed transposed, S^T = K Q^T and O^T = V^T P^T: the
 // keys' rows of S^T come out in the lanes that P^T needs them in, so the
@@ -34,9 +34,11 @@ typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
 constexpr float LN2 = 0.69314718055994530942f;
-// m is moved only when a y passes it by this much: p stays below 2^8, far
-// inside fp16, and most tiles scale nothing.
-constexpr float SLACK = 8.0f;
+// m is moved when a y passes it by this much.  With 32 rows moving costs: p
+// stays below 2^8, far inside fp16, and most tiles scale nothing.  With 16,
+// memory is the bound: the largest p is then 1, which fp16 holds exactly, and
+// a row with one key far above the others keeps all its bits.
+constexpr float slack(int QB) { return QB == 1 ? 0.0f : 8.0f; }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -396,13 +398,14 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
         if (__any(moves)) {
 #pragma unroll
             for (int b = 0; b < QB; ++b) {
-                // Whole steps; a row with no key yet, or with an infinite score, stays.
+                // A row with no key yet, or with an infinite score, stays.
                 const float most = max_over_g(top[b]);
-                const float up = ceilf(most);
-                const bool move = most > thr[b] && fabsf(up) < INFINITY;
-                const float d = move ? up : 0.0f;
-                const float f = move && thr[b] > 0.0f ? exp2_fast(-d) : 1.0f;
-                thr[b] = move ? SLACK : thr[b];
+                const float unit = fabsf(most) < 256.0f ? 32768.0f : 1.0f;
+                const float to = bm[b] - rintf(most * unit) * (1.0f / unit);
+                const bool move = most > thr[b] && fabsf(to) < INFINITY;
+                const float d = move ? bm[b] - to : 0.0f;
+                const float f = move && thr[b] > -INFINITY ? exp2_fast(-d) : 1.0f;
+                thr[b] = move ? slack(QB) : thr[b];
                 bm[b] -= d;
                 l[b] *= f;
 #pragma unroll
@@ -445,7 +448,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
     for (int b = 0; b < QB; ++b) {
         l[b] += __shfl_xor(l[b], 16, 64);
         l[b] += __shfl_xor(l[b], 32, 64);
-        m[b] = thr[b] > 0.0f ? static_cast<float>(KV_EXP_BIAS) - bm[b] : -INFINITY;
+        m[b] = thr[b] > -INFINITY ? static_cast<float>(KV_EXP_BIAS) - bm[b] : -INFINITY;
         // NaN stays in l even where no finite score has moved m.
         if (l[b] != l[b]) m[b] = l[b];
     }

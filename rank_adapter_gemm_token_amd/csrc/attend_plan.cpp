@@ -13,9 +13,41 @@ namespace {
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// Cost of one tile of keys for an item of `rows` query rows, in tenths of the
-// time a tile takes with up to 16.
-int tile_cost(int rows) { return rows <= 16 ? 10 : 16; }
+// All times in tenths of a microsecond, as measured on an MI355X.
+//
+// A tile of 64 keys on a SIMD that two waves share, in which case it is as
+// fast as it gets: the arithmetic of one or two blocks of 16 query rows, or
+// its 16 KB from memory where nobody else reads them (blocks of rows that read
+// the same keys at the same time find them in the L2).
+int tile_cost(int rows, int readers) { return std::max(rows <= 16 ? 9 : 13, 25 / readers); }
+
+// The arithmetic alone, in units of its own.
+int tile_weight(int rows) { return rows <= 16 ? 10 : 16; }
+
+constexpr int CUS = 256, SIMDS = 4 * CUS;
+// What a workgroup takes to begin and to end.
+constexpr double ENDS = 80.0;
+// What a tile takes a wave that waits for nothing but itself.
+constexpr double TILE_ALONE = 15.0;
+
+// How long workgroups of `x` work each (a tile's cost is what it takes two
+// waves of a SIMD) run on a CU that two of them share, and on one of their own.
+double beside(double x) { return x / 2 + ENDS; }
+double alone(double x) { return x / 3 + ENDS; }
+
+// Time of n equal workgroups of x work, two at once on a CU, and of `single`
+// work in waves of their own, which run in what these leave free.
+double launch_time(int64_t n, double x, double single) {
+    const int64_t rest = n % (2 * CUS);
+    double t = static_cast<double>(n / (2 * CUS)) * beside(x);
+    if (rest > 0) {
+        const double last = rest <= CUS ? alone(x) : beside(x);
+        t += last;
+        // Half the slots do 0.7 of what all of them do.
+        single -= 1.4 * last * static_cast<double>(2 * CUS - rest) / (2 * CUS);
+    }
+    return t + std::max(0.0, single);
+}
 
 }  // namespace
 
@@ -30,15 +62,15 @@ AttendPlanner::AttendPlanner(int max_seqs, int max_groups, int max_tokens, int m
     const int gq = n_heads / n_kv_heads;
     // A block has at least one token, of one sequence or of one group.
     max_spans_ = 2 * max_tokens;
-    // plan() gives a span of more than one wave's share ceil(share / 4)
-    // workgroups, and the shares sum to ATTEND_SLOTS / n_kv_heads.
-    const int extra = ceil_div(ATTEND_SLOTS / ATTEND_WAVES, n_kv_heads) + 1;
+    // What splitting may add.
+    const int extra = ceil_div(ATTEND_EXTRA, n_kv_heads) + 1;
+    max_extra_ = extra;
     max_groups_wg_ = max_spans_ + extra;
     // Every span's tokens once, and a block's tokens for each further workgroup.
     max_part_rows_ = 2 * max_tokens + extra * attend_block_tokens(gq);
     items_.reserve(static_cast<size_t>(max_groups_wg_) * ATTEND_WAVES);
     whole_.reserve(static_cast<size_t>(max_groups_wg_));
-    single_.reserve(static_cast<size_t>(max_spans_) + ATTEND_WAVES);
+    single_.reserve(static_cast<size_t>(max_spans_));
     tokens_.reserve(static_cast<size_t>(max_tokens));
     pages_.reserve(static_cast<size_t>(max_pages) + 1);
     spans_.reserve(static_cast<size_t>(max_spans_));
@@ -140,16 +172,18 @@ int AttendPlanner::plan(const AttendBatch &b, const AttendGeometry &geo) {
     }
 
     // Spans, and the tokens that none reaches (nothing to attend to).
-    int64_t cost = 0;
-    auto add_span = [&](int tok0, int n, int page0, int end, int limit0, int step, bool own) {
-        spans_.push_back(Span{tok0, n, page0, end, limit0, step, own, 1});
-        cost += static_cast<int64_t>(ceil_div(end, ATTEND_TILE)) * tile_cost(n * gq);
+    int64_t weight = 0;
+    auto add_span = [&](int tok0, int n, int page0, int end, int limit0, int step, bool own, int readers) {
+        const int tiles = ceil_div(end, ATTEND_TILE), c = tile_cost(n * gq, readers);
+        spans_.push_back(Span{tok0, n, page0, end, limit0, step, own, 0, tiles, static_cast<int64_t>(tiles) * c});
+        weight += static_cast<int64_t>(tiles) * tile_weight(n * gq);
     };
     for (int i = 0; i < b.n_groups; ++i) {
         const int first = i == 0 ? 0 : grp_tok_[i - 1], n = grp_tok_[i] - first;
         if (b.prefix_len[i] == 0) continue;
         for (int t = 0; t < n; t += block)
-            add_span(first + t, std::min(block, n - t), grp_page_[i], b.prefix_len[i], b.prefix_len[i], 0, false);
+            add_span(first + t, std::min(block, n - t), grp_page_[i], b.prefix_len[i], b.prefix_len[i], 0, false,
+                     ceil_div(n, block));
     }
     for (int s = 0; s < b.n_seqs; ++s) {
         const int before = b.kv_len[s] - b.q_len[s];  // query token j sees before + j + 1 of its own
@@ -159,38 +193,71 @@ int AttendPlanner::plan(const AttendBatch &b, const AttendGeometry &geo) {
             const bool prefix = b.group[s] >= 0 && b.prefix_len[b.group[s]] > 0;
             // A block that sees nothing still has its rows to write.
             if (end > 0 || !prefix)
-                add_span(seq_tok_[s] + t, n, seq_page_[s], std::max(0, end), before + t + 1, 1, true);
+                add_span(seq_tok_[s] + t, n, seq_page_[s], std::max(0, end), before + t + 1, 1, true,
+                         ceil_div(b.q_len[s], block));
         }
     }
 
-    // A wave's share of the whole, a tile at least.  A span of up to one share
-    // goes to one wave: its loop is as long as it can be for what it costs to
-    // begin and end.  Longer ones go to whole workgroups, whose waves take
-    // alternating tiles and join in LDS, for two shares a wave: half as many
-    // partial results, and one workgroup of these a CU beside one of the
-    // others (256 sequences on one prefix: 118 us instead of 136; four shares
-    // or one: 123, 141).
-    const int64_t waves = cost * n_kv_heads_;
-    const int64_t share = std::max<int64_t>((waves + ATTEND_SLOTS - 1) / ATTEND_SLOTS, tile_cost(1));
-    const int64_t whole = ATTEND_WAVES * std::max<int64_t>((2 * waves + ATTEND_SLOTS - 1) / ATTEND_SLOTS, tile_cost(1));
+    // A span of up to a wave's share of the whole goes to one wave: its loop is
+    // as long as it can be for what it costs to begin and end.  Longer ones go
+    // to whole workgroups, whose waves take alternating tiles and join in LDS.
+    // The shares are of the arithmetic: beside a prefix that several blocks
+    // read, waves that stream have the memory to themselves (by time, 64
+    // sequences with drafts had most of theirs in workgroups: 60 us, not 52).
+    const int64_t share = std::max<int64_t>(weight * n_kv_heads_ / ATTEND_SLOTS, tile_weight(1));
+    int64_t longest = 0;
+    double stream = 0.0, waits = 0.0;
     for (Span &s : spans_) {
-        const int64_t c = static_cast<int64_t>(ceil_div(s.end, ATTEND_TILE)) * tile_cost(s.n_tok * gq);
-        s.splits = c <= share ? 0 : static_cast<int>((c + whole - 1) / whole);
+        s.splits = static_cast<int64_t>(s.tiles) * tile_weight(s.n_tok * gq) > share ? 1 : 0;
+        if (s.splits)
+            longest = std::max(longest, s.cost);
+        else
+            stream += static_cast<double>(s.cost), waits += TILE_ALONE * s.tiles + ENDS;
+    }
+    const double single = n_kv_heads_ * std::max(stream / SIMDS, waits / ATTEND_SLOTS);
+    // How much of these a workgroup gets: what makes the launch shortest.  (A
+    // fixed share, two a wave, left 320 workgroups for 256 CUs where 480 fit:
+    // 64 sequences with drafts took 52 us.)
+    int64_t best = longest;
+    double best_time = 0.0;
+    for (int k = 1; longest > 0 && k <= 64; k += k < 8 ? 1 : k < 16 ? 2 : 8) {
+        const int64_t x = (longest + k - 1) / k;
+        int64_t n = 0, more = 0;
+        double work = 0.0;
+        bool whole_tiles = true;  // no span in pieces of less than a tile a wave
+        for (const Span &s : spans_)
+            if (s.splits) {
+                const int64_t pieces = (s.cost + x - 1) / x;
+                n += pieces;
+                more += pieces - 1;
+                work += static_cast<double>(s.cost);
+                whole_tiles = whole_tiles && (pieces == 1 || pieces * ATTEND_WAVES <= s.tiles + ATTEND_WAVES - 1);
+            }
+        if (k > 1 && (more >= max_extra_ || !whole_tiles)) break;
+        const double t = launch_time(n * n_kv_heads_, work / static_cast<double>(n), single);
+        if (k == 1 || t < best_time) {
+            best = x;
+            best_time = t;
+        }
+    }
+    for (Span &s : spans_) {
+        if (s.splits) s.splits = static_cast<int>((s.cost + best - 1) / best);
         for (int i = 0; i < s.n_tok; ++i) tokens_[static_cast<size_t>(s.tok0 + i)].n[s.own] = std::max(1, s.splits);
     }
     for (Span &s : spans_) {
         // Alone: no token of the block has a result of another item.
         bool alone = s.splits <= 1;
         for (int i = 0; alone && i < s.n_tok; ++i) alone = tokens_[static_cast<size_t>(s.tok0 + i)].n[!s.own] == 0;
-        const int tiles = ceil_div(s.end, ATTEND_TILE), splits = std::max(1, s.splits);
+        const int tiles = s.tiles, splits = std::max(1, s.splits);
         const int base = part_rows_;
         for (int k = 0; k < splits; ++k) {
             const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * k / splits);
             const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (k + 1) / splits);
             (s.splits > 0 ? whole_ : single_)
-                .push_back(AttendItem{s.tok0, s.n_tok, s.page0, t0 * ATTEND_TILE, std::min(s.end, t1 * ATTEND_TILE),
-                                      s.limit0, (s.step ? ATTEND_STEP : 0) | (s.splits > 0 ? ATTEND_JOINED : 0),
-                                      alone ? -1 : base + k * s.n_tok});
+                .push_back(Piece{{s.tok0, s.n_tok, s.page0, t0 * ATTEND_TILE, std::min(s.end, t1 * ATTEND_TILE), s.limit0,
+                                  (s.step ? ATTEND_STEP : 0) | (s.splits > 0 ? ATTEND_JOINED : 0),
+                                  alone ? -1 : base + k * s.n_tok},
+                                 s.cost / splits});
         }
         for (int i = 0; i < s.n_tok; ++i) {
             AttendToken &t = tokens_[static_cast<size_t>(s.tok0 + i)];
@@ -210,30 +277,29 @@ int AttendPlanner::plan(const AttendBatch &b, const AttendGeometry &geo) {
     }
     // The dearest first, so that what is left at the end is short and the four
     // waves of a workgroup end together.
-    auto dearer = [gq](const AttendItem &x, const AttendItem &y) {
-        const int64_t cx = static_cast<int64_t>(x.end - x.begin) * tile_cost(x.n_tok * gq);
-        const int64_t cy = static_cast<int64_t>(y.end - y.begin) * tile_cost(y.n_tok * gq);
-        if (cx != cy) return cx > cy;
+    auto dearer = [](const Piece &a, const Piece &b) {
+        if (a.cost != b.cost) return a.cost > b.cost;
         // The blocks of rows that read the same keys side by side: they share
         // them in the L2.
+        const AttendItem &x = a.it, &y = b.it;
         if (x.page0 != y.page0) return x.page0 < y.page0;
         return x.begin != y.begin ? x.begin < y.begin : x.tok0 < y.tok0;
     };
     std::sort(whole_.begin(), whole_.end(), dearer);
     std::sort(single_.begin(), single_.end(), dearer);
-    while (single_.size() % ATTEND_WAVES != 0) single_.push_back(AttendItem{});
     // Both kinds side by side over the whole launch: the first is bound by
     // arithmetic where a prefix has many rows, the second by memory.  The
     // blocks of rows that read the same keys stay together.
-    const size_t nw = whole_.size(), ns = single_.size() / ATTEND_WAVES;
+    const size_t nw = whole_.size(), ns = (single_.size() + ATTEND_WAVES - 1) / ATTEND_WAVES;
     for (size_t w = 0, s = 0; w < nw || s < ns;) {
         if (s == ns || (w < nw && w * ns <= s * nw)) {
             do {
-                items_.insert(items_.end(), ATTEND_WAVES, whole_[w++]);
-            } while (w < nw && whole_[w].page0 == whole_[w - 1].page0 && whole_[w].begin == whole_[w - 1].begin);
+                items_.insert(items_.end(), ATTEND_WAVES, whole_[w++].it);
+            } while (w < nw && whole_[w].it.page0 == whole_[w - 1].it.page0 &&
+                     whole_[w].it.begin == whole_[w - 1].it.begin);
         } else {
-            items_.insert(items_.end(), single_.begin() + static_cast<long>(s * ATTEND_WAVES),
-                          single_.begin() + static_cast<long>((s + 1) * ATTEND_WAVES));
+            for (size_t i = s * ATTEND_WAVES; i < (s + 1) * ATTEND_WAVES; ++i)
+                items_.push_back(i < single_.size() ? single_[i].it : AttendItem{});
             ++s;
         }
     }

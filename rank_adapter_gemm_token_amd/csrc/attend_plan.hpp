@@ -55,8 +55,8 @@ constexpr int ATTEND_WAVES = 4;       // waves of a workgroup
 constexpr int ATTEND_MAX_GQ = 32;     // query heads per key/value head
 constexpr int ATTEND_MAX_KEYS = 1 << 30;  // keys of one sequence or prefix (tiles times 64 stay whole 32-bit numbers)
 constexpr int ATTEND_ROWS = 32;       // query rows (tokens x heads of a key head) of an item
-// Waves the work is cut for: two workgroups on each of the 256 CUs.
-constexpr int ATTEND_SLOTS = 2048;
+constexpr int ATTEND_SLOTS = 2048;    // waves that run at once: two workgroups on each of 256 CUs
+constexpr int ATTEND_EXTRA = 1024;    // workgroups that splitting may add, over all key/value heads
 
 // Query tokens of one item, for gq query heads per key/value head.
 inline int attend_block_tokens(int gq) { return gq >= ATTEND_ROWS ? 1 : ATTEND_ROWS / gq; }
@@ -103,13 +103,20 @@ private:
         int tok0, n_tok, page0, end, limit0, step;
         bool own;
         int splits;   // workgroups; 0: one wave
+        int tiles;
+        int64_t cost;
+    };
+    struct Piece {
+        AttendItem it;
+        int64_t cost;
     };
     int check(const AttendBatch &b, const AttendGeometry &geo) const;
     void clear();
 
     int max_seqs_, max_groups_, max_tokens_, max_pages_, n_heads_, n_kv_heads_;
-    int max_spans_, max_groups_wg_, max_part_rows_;
-    std::vector<AttendItem> items_, whole_, single_;
+    int max_spans_, max_extra_, max_groups_wg_, max_part_rows_;
+    std::vector<AttendItem> items_;
+    std::vector<Piece> whole_, single_;  // of a workgroup, of a wave
     std::vector<AttendToken> tokens_;
     std::vector<int32_t> pages_;
     std::vector<Span> spans_;

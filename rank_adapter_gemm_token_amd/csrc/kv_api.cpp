@@ -8,6 +8,7 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <exception>
 #include <new>
 
 #include "../../include/lora.h"
@@ -188,7 +189,7 @@ int lora_attend_plan_create(int max_seqs, int max_groups, int max_tokens, int ma
     lora_attend_plan p = nullptr;
     try {
         p = new lora_attend_plan_s(max_seqs, max_groups, max_tokens, max_pages, n_heads, n_kv_heads);
-    } catch (const std::bad_alloc &) {
+    } catch (const std::exception &) {
         return LORA_ENOMEM;
     }
     p->n_heads = n_heads;

@@ -585,12 +585,13 @@ hipError_t run(const AttendArgs &a, int n_groups, int n_tokens, hipStream_t st) 
     return hipGetLastError();
 }
 
-// Joining in the launch saves the second one (5 us, 16 partial results of one
+// Joining in the launch saves the second one (5 us; 8 partial results of one
 // sequence: 10.0 us instead of 12.5), but each wave then waits for its stores
-// and its count before it ends (4 us); where workgroups follow one another on
-// a CU that is paid several times (64 decoding sequences: 49 us instead of
-// 43).  So: where all of them run at once, two a CU.
-constexpr int JOIN_HERE_WGS = 512;
+// and its count before it ends, which is paid where workgroups share a CU or
+// follow one another on it (64 sequences with drafts, 448 workgroups: 59 us
+// instead of 55; 64 decoding ones, 1200: 49 instead of 43).  So: up to one a
+// CU.
+constexpr int JOIN_HERE_WGS = 256;
 
 template <int DT, int D>
 hipError_t run(const AttendArgs &a, int n_groups, int n_tokens, hipStream_t st) {

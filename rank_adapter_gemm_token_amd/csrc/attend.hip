@@ -65,10 +65,35 @@ __device__ __forceinline__ uint32_t byte_of(const u32x4_t &w, int i) { return (w
 // 2^(byte - 127) (byte 0: 0).
 __device__ __forceinline__ float pow2(uint32_t byte) { return __uint_as_float(byte << 23); }
 
-// The largest of a value held by the lanes r, r + 16, r + 32 and r + 48.
+// The values of lanes r, r + 16, r + 32 and r + 48 joined by op, to all four:
+// neighbouring rows of 16 lanes swap, then the halves of the wave.
+template <typename Op>
+__device__ __forceinline__ float over_g(float v, Op op) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = op(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return op(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
 __device__ __forceinline__ float max_over_g(float v) {
-    v = fmaxf(v, __shfl_xor(v, 16, 64));
-    return fmaxf(v, __shfl_xor(v, 32, 64));
+    return over_g(v, [](float x, float y) { return fmaxf(x, y); });
+}
+
+__device__ __forceinline__ float sum_over_g(float v) {
+    return over_g(v, [](float x, float y) { return x + y; });
+}
+
+// The largest of a value over lanes 16 g .. 16 g + 15 (a row of lanes rotated
+// by 8, 4, 2 and 1).
+__device__ __forceinline__ uint32_t max_over_r(uint32_t v) {
+    auto turned = [](uint32_t x, auto by) {
+        return static_cast<uint32_t>(
+            __builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x120 + decltype(by)::value, 0xf, 0xf, false));
+    };
+    v = max(v, turned(v, std::integral_constant<int, 8>()));
+    v = max(v, turned(v, std::integral_constant<int, 4>()));
+    v = max(v, turned(v, std::integral_constant<int, 2>()));
+    return max(v, turned(v, std::integral_constant<int, 1>()));
 }
 
 // The token (of an item) of a query row: row / gq for row < 64, gq <= 32.
@@ -325,11 +350,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
                 const int key = key0 + 16 * (r >> 2) + 4 * x + (r & 3);
                 top = key < it.end && kb[x] > top ? kb[x] : top;
             }
-#pragma unroll
-            for (int d = 1; d < 16; d <<= 1) {
-                const uint32_t other = __shfl_xor(top, d, 64);
-                top = other > top ? other : top;
-            }
+            top = max_over_r(top);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const int e = static_cast<int>(kb[x]) - static_cast<int>(top) + KV_EXP_BIAS;
@@ -446,8 +467,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
     float m[QB];
 #pragma unroll
     for (int b = 0; b < QB; ++b) {
-        l[b] += __shfl_xor(l[b], 16, 64);
-        l[b] += __shfl_xor(l[b], 32, 64);
+        l[b] = sum_over_g(l[b]);
         m[b] = thr[b] > -INFINITY ? static_cast<float>(KV_EXP_BIAS) - bm[b] : -INFINITY;
         // NaN stays in l even where no finite score has moved m.
         if (l[b] != l[b]) m[b] = l[b];

@@ -34,22 +34,37 @@ __device__ __forceinline__ double weight(float p, float q) {
     return d > 0.0 ? d : 0.0;
 }
 
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
-    return v;
+// v plus what lane data-parallel move CTRL brings to the lanes of the rows in
+// MASK (nothing to the others).
+template <int CTRL, int MASK>
+__device__ __forceinline__ double add_moved(double v) {
+    const uint64_t w = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(w), CTRL, MASK, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(w >> 32), CTRL, MASK, 0xf, false);
+    return v + __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
 
-// Inclusive running sum over the wave's lanes.
+// Inclusive running sum over the wave's lanes, in registers: a sequence's
+// answer waits for five of these one after the other, and by way of LDS each
+// would take 0.3 us.
 __device__ __forceinline__ double wave_scan(double v) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int k = 1; k < 64; k <<= 1) {
-        const double o = __shfl_up(v, k, 64);
-        if (lane >= k) v += o;
-    }
-    return v;
+    v = add_moved<0x111, 0xf>(v);  // row_shr:1
+    v = add_moved<0x112, 0xf>(v);
+    v = add_moved<0x114, 0xf>(v);
+    v = add_moved<0x118, 0xf>(v);
+    v = add_moved<0x142, 0xa>(v);     // lane 15 to the second and fourth row of 16
+    return add_moved<0x143, 0xc>(v);  // lane 31 to the third and fourth
 }
+
+// Lane `l` of v, to all lanes.
+__device__ __forceinline__ double lane_of(double v, int l) {
+    const uint64_t w = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(w), l);
+    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(w >> 32), l);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+__device__ __forceinline__ double wave_sum(double v) { return lane_of(wave_scan(v), 63); }
 
 // Of lanes that hold neighbouring runs' sums v, running r: the first whose
 // running sum passes `aim`, or else the last with any weight.
@@ -146,7 +161,7 @@ __global__ __launch_bounds__(THREADS) void k_verify(VerifyArgs a) {
     }
     const raw *pr = p + static_cast<long>(r0 + kept) * V;
     const raw *qr = kept < n ? q + static_cast<long>(r0 - b + kept) * V : nullptr;
-    const double u_new = static_cast<double>(__shfl(u, kept, 64));
+    const double u_new = static_cast<double>(__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(u), kept)));
 
     // Lane i of part_sum: the sum of part i.
     Part<DT> held;
@@ -193,24 +208,24 @@ __global__ __launch_bounds__(THREADS) void k_verify(VerifyArgs a) {
         at = a.parts - 1;
     }
     double run = wave_scan(part_sum);
-    const double total = __shfl(run, 63, 64), aim = u_new * total;
+    const double total = lane_of(run, 63), aim = u_new * total;
     int token = -1;
     if (total > 0.0 && total <= 1.7976931348623157e308) {
         const int part = pick_lane(part_sum, run, aim);
-        double base = part > 0 ? __shfl(run, part - 1, 64) : 0.0;
+        double base = part > 0 ? lane_of(run, part - 1) : 0.0;
         if (part != at) add_parts(part, part + 1);
         // The segment, by every wave; the rest by the wave that has it.
         const double v = seg[lane];
         run = base + wave_scan(v);
         const int s = pick_lane(v, run, aim);
-        if (s > 0) base = __shfl(run, s - 1, 64);
+        if (s > 0) base = lane_of(run, s - 1);
         if (wave == s % WAVES) {
 #pragma unroll
             for (int k = 0; k < ROUNDS; ++k) {
                 if (k != s / WAVES) continue;
                 const double mine = held.sum(k), upto = base + wave_scan(mine);
                 const int l = pick_lane(mine, upto, aim);
-                if (l > 0) base = __shfl(upto, l - 1, 64);
+                if (l > 0) base = lane_of(upto, l - 1);
                 if (lane == l) {
                     const int i = part * VERIFY_PART + (k * THREADS + t) * STEP;
                     int hit = -1, last = -1;

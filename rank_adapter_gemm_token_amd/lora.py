@@ -446,13 +446,16 @@ def _rows(t, n, heads, dim, dtype, what):
     are contiguous within a token."""
     if t.dtype != dtype or not t.is_cuda:
         raise ValueError("%s: expected a device tensor of %s, got %s on %s" % (what, dtype, t.dtype, t.device))
-    if t.dim() != 3 or t.shape[0] < n or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError("%s: expected [%d, %d, %d], got %s" % (what, n, heads, dim, tuple(t.shape)))
+    shape = t.shape
+    if len(shape) != 3 or shape[0] < n or shape[1] != heads or shape[2] != dim:
+        raise ValueError("%s: expected [%d, %d, %d], got %s" % (what, n, heads, dim, tuple(shape)))
+    if t.is_contiguous():
+        return t.data_ptr(), heads * dim
     st = t.stride()
     if st[2] != 1 or (heads > 1 and st[1] != dim):
         raise ValueError("%s: a token's heads must be contiguous, got strides %s" % (what, st))
     # A single row's stride says nothing.
-    return t.data_ptr(), st[0] if t.shape[0] > 1 else max(st[0], heads * dim)
+    return t.data_ptr(), st[0] if shape[0] > 1 else heads * dim
 
 
 def _flat(t, numel, dtype, what):

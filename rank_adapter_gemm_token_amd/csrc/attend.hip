@@ -20,6 +20,7 @@
 // for the same rows.  Each wave keeps m, l and O of its own keys; the four
 // waves of a workgroup either work on one item and join at the end, or each
 // on an item of its own.
+#include <atomic>
 #include <type_traits>
 
 #include "attend_plan.hpp"
@@ -590,14 +591,22 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
 template <int DT, int D, bool HERE>
 hipError_t run(const AttendArgs &a, int n_groups, int n_tokens, hipStream_t st) {
     constexpr size_t lds = lds_floats(D) * sizeof(float);
-    static const hipError_t set = hipFuncSetAttribute(reinterpret_cast<const void *>(k_attend<DT, D, HERE>),
-                                                      hipFuncAttributeMaxDynamicSharedMemorySize,
-                                                      static_cast<int>(lds));
-    if (set != hipSuccess) return set;
+    // Once a device: the kernel's LDS.
+    static std::atomic<uint64_t> allowed{0};
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if ((allowed.load(std::memory_order_relaxed) & bit) == 0) {
+        e = hipFuncSetAttribute(reinterpret_cast<const void *>(k_attend<DT, D, HERE>),
+                                hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
+        if (e != hipSuccess) return e;
+        allowed.fetch_or(bit, std::memory_order_relaxed);
+    }
     auto grid = [](long n) { return static_cast<unsigned>(n < 1 ? 1 : n > 65536 ? 65536 : n); };
     k_attend<DT, D, HERE><<<grid(static_cast<long>(n_groups) * a.kv_heads), 256, lds, st>>>(a);
     if constexpr (!HERE) {
-        const hipError_t e = hipGetLastError();
+        e = hipGetLastError();
         if (e != hipSuccess) return e;
         const long rows = static_cast<long>(n_tokens) * a.heads, per = 256 / (D / 4);
         k_attend_join<DT, D><<<grid((rows + per - 1) / per), 256, 0, st>>>(a);

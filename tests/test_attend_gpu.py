@@ -223,6 +223,69 @@ def test_a_poisoned_row_is_seen_by_its_readers_alone(dtype):
         assert nan.sum() == 2 * 2 + 1 * 2 + 3 * 2
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_queries_that_are_not_finite_are_alone(dtype):
+    """A NaN or infinite query spoils its own row's output and no other's."""
+    with Step([1, 3, 1], [40, 70, 30], [0, 0, -1], [300], 8, 2, 64, 16, dtype) as s:
+        s.q = s.q.contiguous()
+        clean, lse = s.run()
+        s.check(clean, lse)
+        s.q[2, 5] = float("nan")
+        s.q[4, 0, 3] = float("inf")
+        out, l = s.run()
+        bad = torch.zeros(s.T, s.heads, dtype=torch.bool, device="cuda")
+        bad[2, 5] = bad[4, 0] = True
+        assert out[bad].isnan().all() and l[bad].isnan().all()
+        assert torch.equal(out[~bad], clean[~bad]) and torch.equal(l[~bad], lse[~bad])
+
+
+def test_nothing_to_do():
+    """No sequences, and sequences with nothing new: nothing is written."""
+    with Step([0, 0], [20, 0], [0, -1], [33], 4, 2, 64, 16, "f16", room=4) as s:
+        out, lse = s.run()
+        assert out.numel() == 0
+        i = torch.zeros(0, dtype=torch.int32)
+        lora.lora_attend_plan_set(s.plan, s.kv, i, i, i, i, i)
+        kept = torch.full((2, 4, 64), 7.0, dtype=torch.float16, device="cuda")
+        lora.lora_attend(s.kv, s.plan, kept, 1.0, torch.empty_like(kept))
+        assert (kept == 7).all()
+
+
+def test_pages_past_32_bit_bytes():
+    """A cache of over 4 GiB of keys and of values, a sequence whose pages lie
+    at its ends and around 2^31 and 2^32 bytes."""
+    heads, dim, page = 32, 128, 64
+    per = page * heads * dim
+    n_pages = (1 << 32) // per + 40
+    kv = lora.lora_kv_create(n_pages, page, heads, dim, torch.bfloat16)
+    plan = lora.lora_attend_plan_create(1, 1, 1, 16, heads, heads, dim)
+    try:
+        pages = [0, (1 << 31) // per - 1, (1 << 31) // per, (1 << 32) // per - 1, (1 << 32) // per, n_pages - 1]
+        prefix = [(1 << 32) // per + 7, 5]
+        g = torch.Generator().manual_seed(1)
+        n = (len(pages) + len(prefix)) * page
+        k, v = (torch.randn((n, heads, dim), generator=g).bfloat16() for _ in range(2))
+        slots = [p * page + i for p in prefix + pages for i in range(page)]
+        lora.lora_kv_write(kv, k.cuda(), v.cuda(), torch.tensor(slots, dtype=torch.int32, device="cuda"), n)
+
+        def i32(x):
+            return torch.tensor(x, dtype=torch.int32)
+        lora.lora_attend_plan_set(plan, kv, i32([1]), i32([len(pages) * page]), i32([0]), i32(pages),
+                                  i32([0, len(pages)]), i32([2 * page]), i32(prefix), i32([0, 2]))
+        q = torch.randn((1, heads, dim), generator=g).bfloat16()
+        out, lse = torch.empty_like(q, device="cuda"), torch.empty((1, heads), device="cuda")
+        lora.lora_attend(kv, plan, q.cuda(), dim ** -0.5, out, lse)
+        kk, vv = ref.held_pair(k.double().numpy(), v.double().numpy())
+        want, wl, absv, top, mass = ref.attend(q[0].double().numpy(), (kk, vv), dim ** -0.5)
+        tol, ltol = ref.attend_tolerance(want, absv, top, mass, n, dim, torch.bfloat16)
+        assert (np.abs(out[0].double().cpu().numpy() - want) <= tol).all()
+        assert (np.abs(lse[0].double().cpu().numpy() - wl) <= ltol).all()
+    finally:
+        torch.cuda.synchronize()
+        lora.lora_attend_plan_destroy(plan)
+        lora.lora_kv_destroy(kv)
+
+
 def test_rows_never_written_are_zeros():
     with Step([1, 1], [100, 40], [-1, 0], [33], 2, 1, 64, 16, "f16") as s:
         lora.lora_kv_destroy(s.kv)
@@ -319,6 +382,32 @@ def test_a_graph_follows_the_plan():
             graph.replay()
             torch.cuda.synchronize()
             s.check(out, lse)
+            eager, el = s.run()
+            assert torch.equal(eager, out) and torch.equal(el, lse)
+
+
+def test_a_graph_of_two_launches_follows_the_plan():
+    """As above where the partial results are joined by a second launch."""
+    rng = np.random.default_rng(3)
+    B = 60
+    kv = [int(x) for x in rng.integers(100, 400, B)]
+    with Step([1] * B, kv, [i % 3 - 1 for i in range(B)], [300, 600], 32, 32, 64, 16, "bf16", room=8) as s:
+        s.set_plan()
+        out = torch.empty((s.T, s.heads, s.dim), dtype=s.dtype, device="cuda")
+        lse = torch.empty((s.T, s.heads), device="cuda")
+        st = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(st), torch.cuda.graph(graph, stream=st):
+            lora.lora_attend(s.kv, s.plan, s.q, s.scale, out, lse)
+        for k in (kv, [1] * B, [min(n, 120) for n in kv], kv):
+            s.kv_len = k
+            s.set_plan()
+            torch.cuda.synchronize()
+            out.fill_(7.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            s.check(out, lse, tokens={0, 1, 2, 17, 59})
             eager, el = s.run()
             assert torch.equal(eager, out) and torch.equal(el, lse)
 

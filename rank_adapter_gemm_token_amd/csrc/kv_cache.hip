@@ -87,55 +87,68 @@ __device__ __forceinline__ void quantise(const Words<N> &r, int byte, uint32_t (
 }
 
 // The tokens a workgroup deals with.  It owns 16 neighbouring tokens of the
-// call.  Where 16 neighbours of the call fill a block of 16 rows in order,
-// the block's values are turned in LDS and move as whole words; the workgroup
-// that owns the block's first token takes all of it.  The other tokens it
-// owns move four to a word or a byte at a time (4096 tokens, 32 heads: 22 us
-// in full blocks, 143 us scattered, where every byte has a word of its own).
+// call.  Where most of 16 neighbours of the call lie in order in one block of
+// 16 rows (at least MOST; the others are padding, or of another block), the
+// block's values are turned in LDS and move as words; the workgroup that owns
+// the neighbours' first place takes all of them.  The other tokens it owns
+// move four to a word or a byte at a time (4096 tokens, 32 heads: 23 us in
+// whole blocks, 25 us with 2% padding among them, 137 us scattered, where
+// every byte has a word of its own).
+constexpr int MOST = 9;  // more than half: no two blocks have the same first place
+
 struct Tile {
     int slot;        // of the lane's own token, or -1
-    bool single;     // not part of a full block
+    bool single;     // not moved with a block
     bool word;       // single, one of four neighbours that fill a word of a block
-    int lead;        // first token of the block led from here, or -1 (uniform)
+    int leads;       // bit i: a block is moved from the workgroup's place i (uniform)
     bool any_word;   // of the workgroup's tokens (uniform)
 };
 
-__device__ __forceinline__ Tile find_tile(const int32_t *slots, int n_tokens, int first, int n_rows, int *s) {
-    // s: the slots of tokens first - 15 .. first + 30.
+// The call's slots about the workgroup: tokens first - 15 .. first + 30, and
+// for each place that a block is moved from, the block's first slot.
+struct Window {
+    int s[46];
+    int leads, any_word;
+    int block[TOKENS];
+};
+
+__device__ __forceinline__ Tile find_tile(const int32_t *slots, int n_tokens, int first, int n_rows, Window &w) {
     const int t = threadIdx.x;
     if (t < 46) {
         const int at = first - 15 + t;
-        s[t] = at >= 0 && at < n_tokens ? slots[at] : -1;
+        w.s[t] = at >= 0 && at < n_tokens ? slots[at] : -1;
     }
+    if (t == 0) w.leads = w.any_word = 0;
     __syncthreads();
-    const int me = t / LANES;  // the lane's token: s[15 + me]
+    const int me = t / LANES, l = t % LANES;  // the lane's token: w.s[15 + me]
     Tile r;
-    const int mine = s[15 + me];
+    const int mine = w.s[15 + me];
     r.slot = mine >= 0 && mine < n_rows ? mine : -1;
-    // The block that token `me` would be part of starts `mine % 16` before it.
-    auto full = [&](int lead_at, int slot0) {
-        if (lead_at < 0 || lead_at + 15 >= 46) return false;
-        bool ok = slot0 >= 0 && slot0 <= n_rows - KV_BLOCK;
+    // How many of the 16 neighbours from `place` of the window lie in order in
+    // the block from slot0.
+    auto moved = [&](int place, int slot0) {
+        int n = 0;
 #pragma unroll
-        for (int i = 0; i < KV_BLOCK; ++i) ok &= s[lead_at + i] == slot0 + i;
-        return ok;
+        for (int i = 0; i < KV_BLOCK; ++i) n += w.s[place + i] == slot0 + i;
+        return n >= MOST;
     };
-    r.single = r.slot >= 0 && !full(15 + me - (r.slot & 15), r.slot & ~15);
-    // A token leads when its slot is a block's first; two leaders are at
-    // least 16 tokens apart, so a workgroup has one at most.
-    const bool leads = r.slot >= 0 && (r.slot & 15) == 0 && !r.single;
+    // A token's block begins slot % 16 places before it.
+    const int place = 15 + me - (r.slot & 15);
+    r.single = r.slot >= 0 && !(first - 15 + place >= 0 && moved(place, r.slot & ~15));
     const int w0 = me - (r.slot & 3);
     r.word = r.single && w0 >= 0 && w0 + 3 < TOKENS;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r.word = r.word && s[15 + w0 + i] == (r.slot & ~3) + i;
-    int *lead = s + 46, *any_word = s + 47;
-    if (t == 0) *lead = -1, *any_word = 0;
+    for (int i = 0; i < 4; ++i) r.word = r.word && w.s[15 + w0 + i] == (r.slot & ~3) + i;
+    if (r.word) w.any_word = 1;
+    // Place `me` as a first one: lane l asks for the block of the token l after it.
+    const int other = w.s[15 + me + l], slot0 = other >= l ? other - l : -1;
+    if (slot0 >= 0 && (slot0 & 15) == 0 && slot0 < n_rows && moved(15 + me, slot0)) {
+        w.block[me] = slot0;
+        atomicOr(&w.leads, 1 << me);
+    }
     __syncthreads();
-    if (leads && (t & 15) == 0) *lead = me;
-    if (r.word) *any_word = 1;
-    __syncthreads();
-    r.lead = uniform(*lead);
-    r.any_word = uniform(*any_word) != 0;
+    r.leads = uniform(w.leads);
+    r.any_word = uniform(w.any_word) != 0;
     return r;
 }
 
@@ -151,14 +164,14 @@ __global__ __launch_bounds__(256) void k_kv_write(KvCache c, const uint16_t *k, 
                                                   int64_t v_stride, const int32_t *slots, int n_tokens, int per,
                                                   int groups) {
     constexpr int N = D / LANES;
-    __shared__ int s[48];
+    __shared__ Window w;
     __shared__ __align__(16) uint8_t turned[2][D * VT_LD];
     const int first = static_cast<int>(blockIdx.x) / groups * TOKENS, h0 = static_cast<int>(blockIdx.x) % groups * per;
     const int h1 = h0 + per < c.heads ? h0 + per : c.heads;
     const int me = threadIdx.x / LANES, l = threadIdx.x % LANES;
-    const Tile tile = find_tile(slots, n_tokens, first, c.n_pages << c.page_shift, s);
+    const Tile tile = find_tile(slots, n_tokens, first, c.n_pages << c.page_shift, w);
     if (h0 == 0 && l == 0) {
-        const int mine = s[15 + me];
+        const int mine = w.s[15 + me];
         if (first + me < n_tokens && mine != -1 && tile.slot < 0) atomicAdd(c.err, 1ull);
     }
 
@@ -247,24 +260,45 @@ __global__ __launch_bounds__(256) void k_kv_write(KvCache c, const uint16_t *k, 
         }
         if (tile.any_word) __syncthreads();  // `turned` is written again
     }
-    if (tile.lead < 0) return;
-    const int slot0 = s[15 + tile.lead], token = first + tile.lead + me;
-    Pair x = load(token, h0);
-    for (int head = h0; head < h1; ++head) {
-        const Pair next = load(token, head + 1 < h1 ? head + 1 : head);
-        uint8_t *turn = turned[(head - h0) & 1];
-        uint32_t vw[N / 4];
-        const long R = row_of(c, slot0 + me, head);
-        put(x, R, vw);
+    for (int leads = tile.leads; leads != 0; leads &= leads - 1) {
+        const int place = __builtin_ctz(leads), slot0 = w.block[place], token = first + place + me;
+        int have = 0;  // bit i: row i of the block is among the tokens
 #pragma unroll
-        for (int i = 0; i < N; ++i) turn[(l * N + i) * VT_LD + me] = static_cast<uint8_t>(vw[i / 4] >> (8 * (i % 4)));
-        __syncthreads();
-        // 256 threads x N bytes: the block's D x 16 bytes in order.
-        const int at = threadIdx.x * N, d = at / KV_BLOCK, part = at % KV_BLOCK;
-        uint32_t *vd = reinterpret_cast<uint32_t *>(c.v + (R & ~15L) * D + at);
+        for (int i = 0; i < KV_BLOCK; ++i) have |= (w.s[15 + place + i] == slot0 + i) << i;
+        const bool there = (have >> me) & 1;
+        Pair x{};
+        if (there) x = load(token, h0);
+        for (int head = h0; head < h1; ++head) {
+            Pair next{};
+            uint8_t *turn = turned[(head - h0) & 1];
+            uint32_t vw[N / 4] = {};
+            const long R = row_of(c, slot0, head);
+            if (there) {
+                next = load(token, head + 1 < h1 ? head + 1 : head);
+                put(x, R + me, vw);
+            }
 #pragma unroll
-        for (int i = 0; i < N / 4; ++i) vd[i] = *reinterpret_cast<const uint32_t *>(turn + d * VT_LD + part + 4 * i);
-        x = next;
+            for (int i = 0; i < N; ++i)
+                turn[(l * N + i) * VT_LD + me] = static_cast<uint8_t>(vw[i / 4] >> (8 * (i % 4)));
+            __syncthreads();
+            // 256 threads x N bytes: the block's D x 16 bytes in order.
+            const int at = threadIdx.x * N, d = at / KV_BLOCK, part = at % KV_BLOCK;
+            uint8_t *vd = c.v + R * D + at;
+            const uint8_t *from = turn + d * VT_LD + part;
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+                const int four = (have >> (part + i)) & 15;
+                if (four == 15) {
+                    *reinterpret_cast<uint32_t *>(vd + i) = *reinterpret_cast<const uint32_t *>(from + i);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if ((four >> j) & 1) vd[i + j] = from[i + j];
+                }
+            }
+            x = next;
+        }
+        __syncthreads();  // `turned` is written again
     }
 }
 
@@ -272,12 +306,12 @@ template <int DT, int D>
 __global__ __launch_bounds__(256) void k_kv_read(KvCache c, const int32_t *slots, int n_tokens, uint16_t *k,
                                                  uint16_t *v, int per, int groups) {
     constexpr int N = D / LANES;
-    __shared__ int s[48];
+    __shared__ Window w;
     __shared__ __align__(16) uint8_t turned[2][D * VT_LD];
     const int first = static_cast<int>(blockIdx.x) / groups * TOKENS, h0 = static_cast<int>(blockIdx.x) % groups * per;
     const int h1 = h0 + per < c.heads ? h0 + per : c.heads;
     const int me = threadIdx.x / LANES, l = threadIdx.x % LANES;
-    const Tile tile = find_tile(slots, n_tokens, first, c.n_pages << c.page_shift, s);
+    const Tile tile = find_tile(slots, n_tokens, first, c.n_pages << c.page_shift, w);
 
     // N values of a row: their elements in words w, all scaled by 2^(byte - 127).
     auto put = [&](uint16_t *to, int token, int head, const uint32_t (&w)[N / 4], int byte, bool poison) {
@@ -318,10 +352,10 @@ __global__ __launch_bounds__(256) void k_kv_read(KvCache c, const int32_t *slots
         if (tile.slot < 0) {
             // Nothing is held for this token: an explicit NaN row.
             if (h0 == 0 && l == 0) atomicAdd(c.err, 1ull);
-            const uint32_t w[N / 4] = {};
+            const uint32_t none[N / 4] = {};
             for (int head = h0; head < h1; ++head) {
-                put(k, token, head, w, 0, true);
-                put(v, token, head, w, 0, true);
+                put(k, token, head, none, 0, true);
+                put(v, token, head, none, 0, true);
             }
         } else {
 #pragma unroll 2
@@ -330,29 +364,33 @@ __global__ __launch_bounds__(256) void k_kv_read(KvCache c, const int32_t *slots
                 const Held x = load(R);
                 put(k, token, head, x.k, x.kb, x.vi == KV_POISON);
                 const uint8_t *vs = c.v + (R & ~15L) * D + (R & 15) + l * N * KV_BLOCK;
-                uint32_t w[N / 4] = {};
+                uint32_t e[N / 4] = {};
 #pragma unroll
-                for (int i = 0; i < N; ++i) w[i / 4] |= static_cast<uint32_t>(vs[i * KV_BLOCK]) << (8 * (i % 4));
-                put(v, token, head, w, 2 * KV_EXP_BIAS - x.vi, x.vi == KV_POISON);
+                for (int i = 0; i < N; ++i) e[i / 4] |= static_cast<uint32_t>(vs[i * KV_BLOCK]) << (8 * (i % 4));
+                put(v, token, head, e, 2 * KV_EXP_BIAS - x.vi, x.vi == KV_POISON);
             }
         }
     }
-    if (tile.lead < 0) return;
-    const int token = first + tile.lead + me, slot = s[15 + tile.lead] + me;
-    const int at = threadIdx.x * N, d = at / KV_BLOCK, part = at % KV_BLOCK;
-    Held x = load(row_of(c, slot, h0));
-    for (int head = h0; head < h1; ++head) {
-        const Held next = load(row_of(c, slot, head + 1 < h1 ? head + 1 : head));
-        uint8_t *turn = turned[(head - h0) & 1];
+    for (int leads = tile.leads; leads != 0; leads &= leads - 1) {
+        const int place = __builtin_ctz(leads), slot0 = w.block[place], token = first + place + me;
+        const bool there = w.s[15 + place + me] == slot0 + me;
+        const int at = threadIdx.x * N, d = at / KV_BLOCK, part = at % KV_BLOCK;
+        Held x = load(row_of(c, slot0, h0) + me);
+        for (int head = h0; head < h1; ++head) {
+            const Held next = load(row_of(c, slot0, head + 1 < h1 ? head + 1 : head) + me);
+            uint8_t *turn = turned[(head - h0) & 1];
 #pragma unroll
-        for (int i = 0; i < N / 4; ++i) *reinterpret_cast<uint32_t *>(turn + d * VT_LD + part + 4 * i) = x.v[i];
-        put(k, token, head, x.k, x.kb, x.vi == KV_POISON);
-        __syncthreads();
-        uint32_t w[N / 4] = {};
+            for (int i = 0; i < N / 4; ++i) *reinterpret_cast<uint32_t *>(turn + d * VT_LD + part + 4 * i) = x.v[i];
+            if (there) put(k, token, head, x.k, x.kb, x.vi == KV_POISON);
+            __syncthreads();
+            uint32_t e[N / 4] = {};
 #pragma unroll
-        for (int i = 0; i < N; ++i) w[i / 4] |= static_cast<uint32_t>(turn[(l * N + i) * VT_LD + me]) << (8 * (i % 4));
-        put(v, token, head, w, 2 * KV_EXP_BIAS - x.vi, x.vi == KV_POISON);
-        x = next;
+            for (int i = 0; i < N; ++i)
+                e[i / 4] |= static_cast<uint32_t>(turn[(l * N + i) * VT_LD + me]) << (8 * (i % 4));
+            if (there) put(v, token, head, e, 2 * KV_EXP_BIAS - x.vi, x.vi == KV_POISON);
+            x = next;
+        }
+        __syncthreads();  // `turned` is written again
     }
 }
 

@@ -72,6 +72,17 @@ def slot_list(kind, T, n, page, rng):
     if kind == "pages":        # runs within shuffled pages, as a sequence's tokens lie
         table = rng.permutation(n // page)
         return [int(table[i // page] * page + i % page) for i in range(3, 3 + T)]
+    if kind == "holes":        # blocks with 8, 9 and more of their rows, others' tokens between
+        s, far = [], n - 1
+        for i in range(T):
+            if rng.random() < 0.4 if (i // 32) % 2 else i % 11 == 3:
+                s.append(far if rng.random() < 0.5 else -1)
+                far -= s[-1] == far
+            else:
+                s.append(i)
+        return s
+    if kind == "halves":       # two sequences' halves of blocks in turn, at the same places
+        return [(i // 16) * 32 + (0 if i % 16 < 8 else 16) + i % 16 for i in range(T)]
     # padded: runs with tokens that go nowhere among them
     s = list(range(0, T))
     for i in range(3, T, 7):
@@ -81,11 +92,11 @@ def slot_list(kind, T, n, page, rng):
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("heads,dim,page", [(1, 128, 16), (3, 64, 64), (8, 128, 32)])
-@pytest.mark.parametrize("kind", ["run", "off", "scattered", "pages", "padded"])
+@pytest.mark.parametrize("kind", ["run", "off", "scattered", "pages", "padded", "holes", "halves"])
 @pytest.mark.parametrize("T", [1, 15, 16, 17, 50, 131])
 def test_written_rows_read_back(dtype, heads, dim, page, kind, T):
     rng = np.random.default_rng(T * 7 + heads)
-    n_pages = -(-(T + 40) // page) + 2
+    n_pages = -(-(2 * T + 60) // page) + 2
     with Cache(n_pages, page, heads, dim, dtype) as c:
         slots = slot_list(kind, T, c.n, page, rng)
         # Every slot holds something first: a write must leave the others alone.

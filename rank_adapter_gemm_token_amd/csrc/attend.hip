@@ -20,6 +20,14 @@
 // for the same rows.  Each wave keeps m, l and O of its own keys; the four
 // waves of a workgroup either work on one item and join at the end, or each
 // on an item of its own.
+//
+// What bounds it.  Few rows a key: memory; 64 sequences of 4096 own tokens, 32
+// heads of 128, stream at 6.8 TB/s.  Many rows on one prefix: issue slots; a
+// tile of 64 keys and 32 rows is 476 vector instructions, 64 of them MFMA
+// (each costs 11 issue cycles beside others), about 2480 cycles, of which a
+// SIMD with two waves reaches 3250 (256 sequences on a prefix of 12288: 65 us,
+// 0.8 PFLOP/s).  32 rows fill the 256 registers that leave two waves a SIMD;
+// 16 would widen every element twice as often.
 #include <atomic>
 #include <type_traits>
 
@@ -250,7 +258,8 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
     // are issued one tile ahead, after the scores of the tile before, its
     // values after that tile's second product; the pages of the tile after
     // that are looked up between the two, and first looked at when they are
-    // needed, so that no wait for one of these covers a later one.  Blocks past the end read the last one again.
+    // needed, so that no wait for one of these covers a later one.  Blocks past
+    // the end read the last one again.
     //
     // Keys of few rows have no other reader: they pass the L2 by, which
     // streams faster (64 sequences of 4096 tokens: 6.8 TB/s instead of 6.1)

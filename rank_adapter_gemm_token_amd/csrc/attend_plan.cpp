@@ -235,7 +235,7 @@ int AttendPlanner::plan(const AttendBatch &b, const AttendGeometry &geo) {
             }
         if (k > 1 && (more >= max_extra_ || !whole_tiles)) break;
         const double t = launch_time(n * n_kv_heads_, work / static_cast<double>(n), single);
-        if (k == 1 || t < best_time) {
+        if (k == 1 || t < 0.97 * best_time) {  // more pieces have to be worth it
             best = x;
             best_time = t;
         }

@@ -398,7 +398,6 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
             kp = block_page(kb1 + 4 * step);
             vp = block_page(vb1 + 4 * step);
         }
-        __builtin_amdgcn_sched_barrier(0);
 
         float top[QB];
 #pragma unroll
@@ -406,6 +405,15 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
             const float vi = static_cast<float>(byte_of(vi4, i));
 #pragma unroll
             for (int b = 0; b < QB; ++b) s[i / 4][b][i % 4] = fmaf(s[i / 4][b][i % 4], cs, bm[b] - vi);
+        }
+        if constexpr (more) {
+            // A load after every six of these: in one burst the wave would
+            // stand still for most of them.
+#pragma unroll
+            for (int i = 0; i < 4 * NC + 4; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);  // a read from memory
+                __builtin_amdgcn_sched_group_barrier(0x2, 6, 0);   // VALU
+            }
         }
         if (uniform(key0 + ATTEND_TILE > all)) {
             asm volatile("");  // a branch: as selects it would cost every tile 100 instructions

@@ -103,10 +103,18 @@ int AttendPlanner::check(const AttendBatch &b, const AttendGeometry &geo) const 
     if (b.n_seqs > 0 && (b.q_len == nullptr || b.kv_len == nullptr || b.group == nullptr || b.page0 == nullptr))
         return LORA_EINVAL;
     if (b.n_groups > 0 && (b.prefix_len == nullptr || b.prefix_page0 == nullptr)) return LORA_EINVAL;
+    // Bounds that ascend from 0 or above: no list is looked at past its last one.
+    auto ascend = [](const int32_t *at, int n) {
+        if (n > 0 && at[0] < 0) return false;
+        for (int i = 0; i < n; ++i)
+            if (at[i + 1] < at[i]) return false;
+        return true;
+    };
+    if (!ascend(b.page0, b.n_seqs) || !ascend(b.prefix_page0, b.n_groups)) return LORA_EINVAL;
     int64_t tokens = 0, pages = 0;
     // A row of pages: `len` keys in pages[first .. last).
     auto row = [&](const int32_t *list, const int32_t *at, int i, int32_t len) {
-        if (len < 0 || len > ATTEND_MAX_KEYS || at[i] < 0 || at[i + 1] < at[i]) return false;
+        if (len < 0 || len > ATTEND_MAX_KEYS) return false;
         const int64_t need = (static_cast<int64_t>(len) + geo.page_size - 1) / geo.page_size;
         if (need > at[i + 1] - at[i]) return false;
         if (need > 0 && list == nullptr) return false;

@@ -515,14 +515,17 @@ def lora_attend_plan_set(plan, kv, q_len, kv_len, group, pages, page0, prefix_le
             raise ValueError("%s: expected %d contiguous host int32 elements, got %s of %s on %s"
                              % (what, n, tuple(t.shape), t.dtype, t.device))
         return t.data_ptr()
+    def lists(entries, first, n, what, first_what):
+        """The entries, as many as their last bound says, and the n + 1 bounds
+        (a longer tensor's further ones are not looked at)."""
+        at = host(first, n + 1 if n else 0, first_what)
+        return host(entries, int(first[n]) if n else 0, what), at
     n_seqs = q_len.numel()
     n_groups = 0 if prefix_len is None else prefix_len.numel()
     b = lora_attend_batch(n_seqs, n_groups, host(q_len, n_seqs, "q_len"), host(kv_len, n_seqs, "kv_len"),
-                          host(group, n_seqs, "group"),
-                          host(pages, int(page0[-1]) if n_seqs else 0, "pages"),
-                          host(page0, n_seqs + 1 if n_seqs else 0, "page0"), host(prefix_len, n_groups, "prefix_len"),
-                          host(prefix_pages, int(prefix_page0[-1]) if n_groups else 0, "prefix_pages"),
-                          host(prefix_page0, n_groups + 1 if n_groups else 0, "prefix_page0"))
+                          host(group, n_seqs, "group"), *lists(pages, page0, n_seqs, "pages", "page0"),
+                          host(prefix_len, n_groups, "prefix_len"),
+                          *lists(prefix_pages, prefix_page0, n_groups, "prefix_pages", "prefix_page0"))
     _attend_plans[plan][2] = 0
     _check(_lib.lora_attend_plan_set(plan, kv, ctypes.byref(b), _stream(stream)), "lora_attend_plan_set")
     _attend_plans[plan][2] = int(q_len.sum())

@@ -557,6 +557,8 @@ def lora_verify(verifier, p_target, p_draft, draft, row0, u, n_seqs, n_rows, tok
     vocab, dtype = p_target.shape[-1], p_target.dtype
     n_drafts = max(0, n_rows - n_seqs)
     i32 = torch.int32
+    if n_drafts > 0 and p_draft.shape[-1] != vocab:
+        raise ValueError("p_draft: expected rows of the target's vocabulary, %d, got %s" % (vocab, tuple(p_draft.shape)))
     _check(_lib.lora_verify(verifier, _flat(p_target, n_rows * vocab, dtype, "p_target"),
                             _flat(p_draft, n_drafts * vocab, dtype, "p_draft"), DTYPE_OF[dtype], vocab,
                             _flat(draft, n_drafts, i32, "draft"), _flat(row0, n_seqs + 1, i32, "row0"),

@@ -44,3 +44,17 @@ def test_bounds_are_looked_at_after_their_type_is(no_plan):
         with pytest.raises(ValueError, match="prefix_page0"):
             lora.lora_attend_plan_set(no_plan, None, one, one, one, i32(1, 2, 3, 4), i32(0, 2, 4), one,
                                       i32(1, 2, 3, 4), page0)
+
+
+def test_the_draft_has_the_target_s_vocabulary():
+    """Rows of another length would be read at the wrong stride.  Without
+    drafted tokens the draft is not looked at."""
+    p, i = torch.zeros(4, 64), i32(0, 0, 0, 0)
+    for wrong in (torch.zeros(2, 96), torch.zeros(4, 32), torch.zeros(128)):
+        with pytest.raises(ValueError, match="p_draft: .* vocabulary"):
+            lora.lora_verify(None, p, wrong, i, i, p, 2, 4, i, i, stream=0)
+    for q in (torch.zeros(2, 64), torch.zeros(1, 2, 64)):
+        with pytest.raises(ValueError, match="p_target: .* on the device"):
+            lora.lora_verify(None, p, q, i, i, p, 2, 4, i, i, stream=0)
+    with pytest.raises(ValueError, match="p_target: .* on the device"):
+        lora.lora_verify(None, p, torch.zeros(0, 7), i, i, p, 4, 4, i, i, stream=0)

@@ -70,10 +70,13 @@ __device__ __forceinline__ double lane_of(double v, int l) {
 
 __device__ __forceinline__ double wave_sum(double v) { return lane_of(wave_scan(v), 63); }
 
-// Of lanes that hold neighbouring runs' sums v, running r: the first whose
-// running sum passes `aim`, or else the last with any weight.
+// Of lanes that hold neighbouring runs' sums v, running r: the first with any
+// weight whose running sum passes `aim`, or else the last with any weight.  (A
+// lane of none may be the first to pass: the scan adds the same weights in
+// another order for each lane, so its sum may stand a rounding above its left
+// neighbour's.)
 __device__ __forceinline__ int pick_lane(double v, double r, double aim) {
-    const unsigned long long passes = __ballot(r > aim), some = __ballot(v > 0.0);
+    const unsigned long long some = __ballot(v > 0.0), passes = __ballot(r > aim) & some;
     return uniform(passes ? __builtin_ctzll(passes) : some ? 63 - __builtin_clzll(some) : 0);
 }
 

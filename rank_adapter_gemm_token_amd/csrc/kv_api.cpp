@@ -237,15 +237,16 @@ int lora_attend_plan_destroy(lora_attend_plan plan) {
 }
 
 int lora_attend_plan_set(lora_attend_plan plan, lora_kv kv, const lora_attend_batch *batch, void *stream) {
-    if (plan == nullptr || kv == nullptr || batch == nullptr) return LORA_EINVAL;
+    if (plan == nullptr) return LORA_EINVAL;
+    std::lock_guard<std::mutex> lk(plan->mu);
+    plan->set = false;  // until this batch is on its way, whatever refuses it
+    if (kv == nullptr || batch == nullptr) return LORA_EINVAL;
     if (kv->device != plan->device || kv->c.heads != plan->n_kv_heads || kv->c.dim != plan->head_dim)
         return LORA_EMISMATCH;
-    std::lock_guard<std::mutex> lk(plan->mu);
     const lora::AttendBatch b{batch->n_seqs, batch->n_groups, batch->q_len, batch->kv_len, batch->group,
                               batch->pages, batch->page0, batch->prefix_len, batch->prefix_pages,
                               batch->prefix_page0};
     const lora::AttendGeometry geo{plan->n_heads, plan->n_kv_heads, kv->page_size, kv->c.n_pages};
-    plan->set = false;
     const int rc = plan->planner.plan(b, geo);
     if (rc != LORA_OK) return rc;
     DeviceGuard g(plan->device);

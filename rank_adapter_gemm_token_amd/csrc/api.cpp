@@ -31,7 +31,14 @@ thread_local std::string g_last_hip;
 
 int lora::hip_fail(hipError_t e) {
     g_last_hip = hipGetErrorString(e);
+    (void)hipGetLastError();
     return LORA_EHIP;
+}
+
+int lora::alloc_status(hipError_t e) {
+    if (e != hipErrorOutOfMemory) return hip_fail(e);
+    (void)hipGetLastError();
+    return LORA_ENOMEM;
 }
 
 namespace {
@@ -624,8 +631,7 @@ int lora_pool_create(int d_in, int d_out, int max_rank, int n_slots, int max_tok
     if (e == hipSuccess) e = hipMalloc(&p->B_slab, b_bytes);
     if (e == hipSuccess) e = hipMalloc(reinterpret_cast<void **>(&p->slots_dev), S * sizeof(lora::SlotDev));
     if (e == hipSuccess) e = hipMalloc(reinterpret_cast<void **>(&p->ws), ws_bytes);
-    if (e == hipErrorOutOfMemory) return fail(LORA_ENOMEM);
-    if (e != hipSuccess) return fail(hip_fail(e));
+    if (e != hipSuccess) return fail(lora::alloc_status(e));
     p->device_bytes = a_bytes + b_bytes + S * sizeof(lora::SlotDev) + ws_bytes;
 
     e = hipStreamCreateWithFlags(&p->internal, hipStreamNonBlocking);
@@ -866,7 +872,7 @@ int lora_plan_create(int max_tokens, int n_slots, lora_plan *out) {
     if (e == hipSuccess) e = hipStreamSynchronize(pl->internal);
     if (e == hipSuccess) e = hipEventCreateWithFlags(&pl->done, kCompletionEventFlags);
     if (e != hipSuccess) {
-        const int rc = (e == hipErrorOutOfMemory) ? LORA_ENOMEM : hip_fail(e);
+        const int rc = lora::alloc_status(e);
         lora_plan_destroy(pl);
         return rc;
     }
@@ -979,7 +985,7 @@ int lora_loader_create(uint64_t capacity_bytes, lora_loader *out) {
     }
     if (e == hipSuccess) e = hipStreamCreateWithFlags(&l->copy, hipStreamNonBlocking);
     if (e != hipSuccess) {
-        const int rc = (e == hipErrorOutOfMemory) ? LORA_ENOMEM : hip_fail(e);
+        const int rc = lora::alloc_status(e);
         lora_loader_destroy(l);
         return rc;
     }

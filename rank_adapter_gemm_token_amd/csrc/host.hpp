@@ -9,8 +9,14 @@
 namespace lora {
 
 // Keeps the HIP error's text for lora_last_hip_error and returns LORA_EHIP
-// (defined in api.cpp).
+// (defined in api.cpp).  The runtime remembers a failed call until it is asked
+// for its last error: it is asked here, or the check after the next launch
+// would report this call's failure as the launch's.
 int hip_fail(hipError_t e);
+
+// The status of a failed call that allocates: LORA_ENOMEM where that was the
+// reason.
+int alloc_status(hipError_t e);
 
 #define HIP_TRY(expr)                                    \
     do {                                                 \

@@ -17,6 +17,7 @@
 #include "kv_internal.hpp"
 
 using lora::align_up;
+using lora::alloc_status;
 using lora::aligned;
 using lora::DeviceGuard;
 using lora::hip_fail;
@@ -62,8 +63,6 @@ struct lora_verifier_s {
 namespace {
 
 bool dim_ok(int d) { return d == 64 || d == 128; }
-
-int alloc_status(hipError_t e) { return e == hipErrorOutOfMemory ? LORA_ENOMEM : hip_fail(e); }
 
 // Waits for the device's work and frees `mem` on its device.
 int free_on(int device, char *mem) {

@@ -505,7 +505,11 @@ int lora_attend_plan_destroy(lora_attend_plan plan);
  * LORA_EMISMATCH; the plan is then empty until the next one.
  * Plan and attention share the plan's memory: calls on one plan on different
  * streams are ordered by the caller.  A captured lora_attend reads the plan as
- * it is when the graph runs, so a graph may be replayed after a new plan. */
+ * it is when the graph runs, so a graph may be replayed after a new plan, of
+ * any number of tokens up to max_tokens: the captured q, out and lse need room
+ * for the most that it will meet, and rows past the plan's tokens are not
+ * written.  The launch is as large as the plan at capture asks for (one of no
+ * tokens: fills the device), so capture with the most work, or with none. */
 int lora_attend_plan_set(lora_attend_plan plan, lora_kv kv, const lora_attend_batch *batch, void *stream);
 
 /* out = softmax(scale * q k^T) v for the planned batch, the values as the cache
@@ -519,6 +523,8 @@ int lora_attend_plan_set(lora_attend_plan plan, lora_kv kv, const lora_attend_ba
  *   lse    device float [tokens][n_heads], log(sum(exp(scale * q k^T))), or NULL
  * Scores, maxima, sums and outputs are held in fp32; the weights are rounded
  * to fp16 (11 bits) for the product with the values, the output once.
+ * A plan of no tokens: nothing is enqueued, and q, out and lse are not looked
+ * at, unless the stream is being captured.
  * Errors (nothing enqueued): LORA_EINVAL (no plan set, pointers, strides, scale
  * not finite), LORA_EMISMATCH, LORA_EHIP. */
 int lora_attend(lora_kv kv, lora_attend_plan plan, const void *q, int64_t q_stride, float scale, void *out,

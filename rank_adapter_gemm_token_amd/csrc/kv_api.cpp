@@ -34,7 +34,7 @@ struct lora_kv_s {
 
 struct lora_attend_plan_s {
     int device = 0;
-    int n_heads = 0, n_kv_heads = 0, head_dim = 0;
+    int max_tokens = 0, n_heads = 0, n_kv_heads = 0, head_dim = 0;
     lora::AttendPlanner planner;
     char *mem = nullptr;                    // the plan as the kernels read it, then the partial results
     float *part_o = nullptr, *part_ml = nullptr;
@@ -191,6 +191,7 @@ int lora_attend_plan_create(int max_seqs, int max_groups, int max_tokens, int ma
     } catch (const std::exception &) {
         return LORA_ENOMEM;
     }
+    p->max_tokens = max_tokens;
     p->n_heads = n_heads;
     p->n_kv_heads = n_kv_heads;
     p->head_dim = head_dim;
@@ -275,13 +276,21 @@ int lora_attend(lora_kv kv, lora_attend_plan plan, const void *q, int64_t q_stri
     if (kv->device != plan->device || kv->c.heads != plan->n_kv_heads || kv->c.dim != plan->head_dim ||
         kv->page_size != plan->page_size || kv->c.n_pages != plan->n_pages)
         return LORA_EMISMATCH;
-    const int n_tokens = static_cast<int>(plan->planner.tokens().size());
-    if (n_tokens == 0) return LORA_OK;
+    int n_tokens = static_cast<int>(plan->planner.tokens().size()), n_groups = plan->planner.groups();
+    DeviceGuard g(plan->device);
+    HIP_TRY(g.error());
+    if (n_tokens == 0) {
+        // Nothing to do now, but a graph that captures the call may be
+        // replayed after plans of any size: launched to fill the device.
+        hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
+        HIP_TRY(hipStreamIsCapturing(static_cast<hipStream_t>(stream), &cap));
+        if (cap == hipStreamCaptureStatusNone) return LORA_OK;
+        n_tokens = plan->max_tokens;
+        n_groups = (lora::ATTEND_SLOTS / lora::ATTEND_WAVES + plan->n_kv_heads - 1) / plan->n_kv_heads;
+    }
     const int64_t row = static_cast<int64_t>(plan->n_heads) * plan->head_dim;
     if (q == nullptr || out == nullptr || q == out || q_stride < row || q_stride % 8 != 0) return LORA_EINVAL;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return LORA_EINVAL;
-    DeviceGuard g(plan->device);
-    HIP_TRY(g.error());
     lora::AttendArgs a{};
     a.meta = plan->mem;
     a.k = kv->c.k;
@@ -302,7 +311,7 @@ int lora_attend(lora_kv kv, lora_attend_plan plan, const void *q, int64_t q_stri
     a.page_shift = kv->c.page_shift;
     a.n_pages = kv->c.n_pages;
     a.scale = scale * 1.44269504088896340736f;
-    HIP_TRY(lora::launch_attend(a, kv->c.dtype, plan->head_dim, plan->planner.groups(), n_tokens,
+    HIP_TRY(lora::launch_attend(a, kv->c.dtype, plan->head_dim, n_groups, n_tokens,
                                 static_cast<hipStream_t>(stream)));
     return LORA_OK;
 }

@@ -54,3 +54,68 @@ def test_every_refusal_leaves_no_plan():
         finally:
             lora.lora_kv_destroy(wide)
             lora.lora_kv_destroy(more)
+
+
+class Captured:
+    """lora_attend of `s` captured with the plan that is set, on buffers of the
+    step's first size, and 7 wherever it has not written."""
+
+    def __init__(self, s):
+        self.s = s
+        self.out = torch.empty((s.T, s.heads, s.dim), dtype=s.dtype, device="cuda")
+        self.lse = torch.empty((s.T, s.heads), device="cuda")
+        st = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        self.graph = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(st), torch.cuda.graph(self.graph, stream=st):
+            lora.lora_attend(s.kv, s.plan, s.q, s.scale, self.out, self.lse)
+
+    def replay(self):
+        torch.cuda.synchronize()
+        self.out.fill_(7.0)
+        self.lse.fill_(7.0)
+        self.graph.replay()
+        torch.cuda.synchronize()
+
+    def check(self):
+        """The planned tokens' rows, and none past them."""
+        self.replay()
+        n = sum(self.s.q_len)
+        self.s.check(self.out, self.lse)
+        assert (self.out[n:] == 7).all() and (self.lse[n:] == 7).all()
+
+
+@pytest.mark.parametrize("first", [[0, 0, 0], [4, 3, 2], [0, 1, 0]])
+@pytest.mark.parametrize("heads,kv_heads", [(4, 2), (128, 64)])
+def test_a_graph_follows_plans_of_other_token_counts(first, heads, kv_heads):
+    """From none to as many as the buffers hold, captured at either end."""
+    with Step([4, 3, 2], [100, 300, 50], [0, 0, -1], [500], heads, kv_heads, 64, 16, "f16", room=8) as s:
+        s.q_len = first
+        s.set_plan()
+        g = Captured(s)
+        for n in ([4, 3, 2], [1, 0, 2], [0, 0, 0], [4, 3, 2], first):
+            s.q_len = n
+            s.set_plan()
+            g.check()
+            g.check()  # and once more on the same plan
+
+
+def test_a_capture_without_tokens_asks_for_its_buffers():
+    """They are what later plans' tokens are read from and written to."""
+    lib, f = lora.raw_lib(), ctypes.c_float
+    with Step([2], [40], [-1], [], 4, 2, 64, 16, "f16") as s:
+        out = torch.full((2, 4, 64), 7.0, dtype=torch.float16, device="cuda")
+        s.q_len = [0]
+        s.set_plan()
+        args = [(s.q.data_ptr(), out.data_ptr()), (None, out.data_ptr()), (s.q.data_ptr(), None)]
+        # Not captured: nothing to do, and nothing asked for.
+        assert [lib.lora_attend(s.kv, s.plan, q, 320, f(1), o, None, None) for q, o in args] == [lora.LORA_OK] * 3
+        st = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(st), torch.cuda.graph(graph, stream=st):
+            got = [lib.lora_attend(s.kv, s.plan, q, 320, f(1), o, None, st.cuda_stream) for q, o in args]
+        assert got == [lora.LORA_OK, lora.LORA_EINVAL, lora.LORA_EINVAL]
+        graph.replay()
+        torch.cuda.synchronize()
+        assert (out == 7).all()

@@ -509,7 +509,9 @@ int lora_attend_plan_destroy(lora_attend_plan plan);
  * any number of tokens up to max_tokens: the captured q, out and lse need room
  * for the most that it will meet, and rows past the plan's tokens are not
  * written.  The launch is as large as the plan at capture asks for (one of no
- * tokens: fills the device), so capture with the most work, or with none. */
+ * tokens: fills the device), so capture with the most work, or with none.  A
+ * replay on a cache of another page size or count than the plan's writes NaN
+ * for the plan's tokens. */
 int lora_attend_plan_set(lora_attend_plan plan, lora_kv kv, const lora_attend_batch *batch, void *stream);
 
 /* out = softmax(scale * q k^T) v for the planned batch, the values as the cache

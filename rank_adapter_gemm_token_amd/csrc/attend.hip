@@ -569,6 +569,18 @@ __device__ __forceinline__ bool plan_fits(const AttendArgs &a, const AttendHeade
     return h->page_size == 1 << a.page_shift && h->n_pages == a.n_pages;
 }
 
+// NaN for the plan's tokens, whose outputs are not computed.
+template <int DT>
+__device__ __forceinline__ void put_nan(const AttendArgs &a, int n_tokens, int dim) {
+    const long rows = static_cast<long>(n_tokens) * a.heads, threads = static_cast<long>(gridDim.x) * 256;
+    const long at = static_cast<long>(blockIdx.x) * 256 + threadIdx.x;
+    constexpr uint32_t nan = Elem<DT>::qnan * 0x10001u;
+    for (long i = at; i < rows * dim / 8; i += threads)
+        *reinterpret_cast<u32x4_t *>(a.out + i * 8) = u32x4_t{nan, nan, nan, nan};
+    if (a.lse != nullptr)
+        for (long i = at; i < rows; i += threads) a.lse[i] = __uint_as_float(Elem<DT_F32>::qnan);
+}
+
 template <int DT, int D, bool HERE>
 __global__ __launch_bounds__(256, 2) void k_attend(AttendArgs a) {
     extern __shared__ float lds[];
@@ -576,7 +588,8 @@ __global__ __launch_bounds__(256, 2) void k_attend(AttendArgs a) {
     const AttendItem *items = reinterpret_cast<const AttendItem *>(a.meta + sizeof(AttendHeader));
     const AttendToken *toks = reinterpret_cast<const AttendToken *>(a.meta + h->token_off);
     const int32_t *pages = reinterpret_cast<const int32_t *>(a.meta + h->page_off);
-    const int n = plan_fits(a, h) ? h->n_groups * a.kv_heads : 0;
+    if (!plan_fits(a, h)) return put_nan<DT>(a, h->n_tokens, D);
+    const int n = h->n_groups * a.kv_heads;
     const int wave = uniform(threadIdx.x >> 6);
     for (int w = blockIdx.x; w < n; w += gridDim.x) {
         const int i = w / a.kv_heads, kvh = w - i * a.kv_heads;

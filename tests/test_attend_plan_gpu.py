@@ -119,3 +119,30 @@ def test_a_capture_without_tokens_asks_for_its_buffers():
         graph.replay()
         torch.cuda.synchronize()
         assert (out == 7).all()
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim,dtype", [(4, 2, 64, "f16"), (128, 64, 128, "bf16")])
+def test_a_replay_on_a_cache_that_the_plan_is_not_for_is_nan(heads, kv_heads, dim, dtype):
+    """Its pages are another cache's: they are not followed, and what is not
+    computed does not look like an output."""
+    with Step([4, 3, 2], [100, 300, 50], [0, 0, -1], [500], heads, kv_heads, dim, 16, dtype, room=8) as s:
+        s.set_plan()
+        g = Captured(s)
+        g.check()
+        more = lora.lora_kv_create(s.n_pages + 1, 16, kv_heads, dim, s.dtype)
+        longer = lora.lora_kv_create(s.n_pages, 32, kv_heads, dim, s.dtype)
+        try:
+            for kv in (more, longer):
+                for n in ([4, 3, 2], [1, 0, 2], [0, 0, 0]):
+                    s.q_len = n
+                    lora.lora_attend_plan_set(s.plan, kv, **s.lists())
+                    g.replay()
+                    T = sum(n)
+                    assert g.out[:T].isnan().all() and g.lse[:T].isnan().all()
+                    assert (g.out[T:] == 7).all() and (g.lse[T:] == 7).all()
+                s.q_len = [4, 3, 2]
+                s.set_plan()
+                g.check()
+        finally:
+            lora.lora_kv_destroy(more)
+            lora.lora_kv_destroy(longer)

@@ -502,7 +502,8 @@ int lora_attend_plan_destroy(lora_attend_plan plan);
  * Every list is checked first: lengths below 0, groups and page ids out of
  * range, fewer pages than a length needs are LORA_EINVAL, more new tokens
  * than max_tokens LORA_ETOKENS, a cache of other heads or head_dim
- * LORA_EMISMATCH; the plan is then empty until the next one.
+ * LORA_EMISMATCH; the plan is then empty until the next one, and so is the
+ * device's, except after a refusal during a capture, when nothing can be sent.
  * Plan and attention share the plan's memory: calls on one plan on different
  * streams are ordered by the caller.  A captured lora_attend reads the plan as
  * it is when the graph runs, so a graph may be replayed after a new plan, of
@@ -511,7 +512,8 @@ int lora_attend_plan_destroy(lora_attend_plan plan);
  * written.  The launch is as large as the plan at capture asks for (one of no
  * tokens: fills the device), so capture with the most work, or with none.  A
  * replay on a cache of another page size or count than the plan's writes NaN
- * for the plan's tokens. */
+ * for the plan's tokens, and one after a refused plan for those of the last
+ * plan that was not refused. */
 int lora_attend_plan_set(lora_attend_plan plan, lora_kv kv, const lora_attend_batch *batch, void *stream);
 
 /* out = softmax(scale * q k^T) v for the planned batch, the values as the cache

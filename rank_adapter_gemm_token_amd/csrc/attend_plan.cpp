@@ -332,4 +332,12 @@ size_t AttendPlanner::write(void *to) const {
     return static_cast<size_t>(h.page_off) + pages_.size() * 4;
 }
 
+size_t AttendPlanner::write_none(void *to, int n_tokens) {
+    AttendHeader h{};
+    h.n_tokens = n_tokens;
+    h.token_off = h.page_off = static_cast<int32_t>(sizeof h);
+    std::memcpy(to, &h, sizeof h);
+    return sizeof h;
+}
+
 }  // namespace lora

@@ -91,6 +91,10 @@ public:
     // The bytes the device reads, max_bytes() at most; returns how many.
     size_t write(void *to) const;
 
+    // As write(): a plan of no work, for no cache (of 0 pages), of n_tokens
+    // tokens, for which the device writes NaN.
+    static size_t write_none(void *to, int n_tokens);
+
     const std::vector<AttendItem> &items() const { return items_; }  // four a workgroup
     int groups() const { return static_cast<int>(items_.size()) / ATTEND_WAVES; }
     const std::vector<AttendToken> &tokens() const { return tokens_; }

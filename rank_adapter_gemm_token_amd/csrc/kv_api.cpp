@@ -45,6 +45,7 @@ struct lora_attend_plan_s {
     hipEvent_t sent[2] = {nullptr, nullptr};
     int next = 0;
     bool set = false;
+    int sent_tokens = -1;  // of the last plan that went to the device; -1: none did
     int page_size = 0, n_pages = 0;
     std::mutex mu;
 
@@ -79,6 +80,17 @@ void free_plan(lora_attend_plan p) {
         if (p->sent[i]) (void)hipEventDestroy(p->sent[i]);
     }
     if (p->mem) (void)hipFree(p->mem);
+}
+
+// Checks and cuts a batch on the host.
+int plan_batch(lora_attend_plan plan, lora_kv kv, const lora_attend_batch *batch) {
+    if (kv == nullptr || batch == nullptr) return LORA_EINVAL;
+    if (kv->device != plan->device || kv->c.heads != plan->n_kv_heads || kv->c.dim != plan->head_dim)
+        return LORA_EMISMATCH;
+    const lora::AttendBatch b{batch->n_seqs, batch->n_groups, batch->q_len, batch->kv_len, batch->group,
+                              batch->pages, batch->page0, batch->prefix_len, batch->prefix_pages,
+                              batch->prefix_page0};
+    return plan->planner.plan(b, lora::AttendGeometry{plan->n_heads, plan->n_kv_heads, kv->page_size, kv->c.n_pages});
 }
 
 }  // namespace
@@ -240,15 +252,6 @@ int lora_attend_plan_set(lora_attend_plan plan, lora_kv kv, const lora_attend_ba
     if (plan == nullptr) return LORA_EINVAL;
     std::lock_guard<std::mutex> lk(plan->mu);
     plan->set = false;  // until this batch is on its way, whatever refuses it
-    if (kv == nullptr || batch == nullptr) return LORA_EINVAL;
-    if (kv->device != plan->device || kv->c.heads != plan->n_kv_heads || kv->c.dim != plan->head_dim)
-        return LORA_EMISMATCH;
-    const lora::AttendBatch b{batch->n_seqs, batch->n_groups, batch->q_len, batch->kv_len, batch->group,
-                              batch->pages, batch->page0, batch->prefix_len, batch->prefix_pages,
-                              batch->prefix_page0};
-    const lora::AttendGeometry geo{plan->n_heads, plan->n_kv_heads, kv->page_size, kv->c.n_pages};
-    const int rc = plan->planner.plan(b, geo);
-    if (rc != LORA_OK) return rc;
     DeviceGuard g(plan->device);
     HIP_TRY(g.error());
     hipStream_t st = static_cast<hipStream_t>(stream);
@@ -256,12 +259,19 @@ int lora_attend_plan_set(lora_attend_plan plan, lora_kv kv, const lora_attend_ba
     hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
     HIP_TRY(hipStreamIsCapturing(st, &cap));
     if (cap != hipStreamCaptureStatusNone) return LORA_EINVAL;
+    const int rc = plan_batch(plan, kv, batch);
+    // A refused batch leaves the device a plan for no cache, so that graphs do
+    // not attend to the one before.
+    if (rc != LORA_OK && plan->sent_tokens < 0) return rc;
     const int i = plan->next;
     HIP_TRY(hipEventSynchronize(plan->sent[i]));  // done at once unless two plans are still on their way
-    const size_t bytes = plan->planner.write(plan->host[i]);
+    const size_t bytes = rc == LORA_OK ? plan->planner.write(plan->host[i])
+                                       : lora::AttendPlanner::write_none(plan->host[i], plan->sent_tokens);
     HIP_TRY(hipMemcpyAsync(plan->mem, plan->host[i], bytes, hipMemcpyHostToDevice, st));
     HIP_TRY(hipEventRecord(plan->sent[i], st));
     plan->next = 1 - i;
+    if (rc != LORA_OK) return rc;
+    plan->sent_tokens = static_cast<int>(plan->planner.tokens().size());
     plan->page_size = kv->page_size;
     plan->n_pages = kv->c.n_pages;
     plan->set = true;

@@ -146,3 +146,60 @@ def test_a_replay_on_a_cache_that_the_plan_is_not_for_is_nan(heads, kv_heads, di
         finally:
             lora.lora_kv_destroy(more)
             lora.lora_kv_destroy(longer)
+
+
+def test_a_replay_after_a_refused_plan_is_nan():
+    """The batch before is not attended to again -- its pages may have gone to
+    others by then -- nor do its outputs stay as if they were new."""
+    with Step([4, 3, 2], [100, 300, 50], [0, 0, -1], [500], 4, 2, 64, 16, "f16", room=8) as s:
+        s.set_plan()
+        g = Captured(s)
+        wide = lora.lora_kv_create(s.n_pages, 16, 2, 128, torch.float16)
+        try:
+            for n in ([4, 3, 2], [1, 0, 2]):
+                for kv, lists in [(s.kv, dict(kv_len=torch.tensor([100, 300, -1], dtype=torch.int32))), (wide, {}),
+                                  (None, {})]:
+                    s.q_len = n
+                    s.set_plan()
+                    g.check()
+                    with pytest.raises(lora.LoraError):
+                        lora.lora_attend_plan_set(s.plan, kv, **dict(s.lists(), **lists))
+                    for _ in range(2):
+                        g.replay()
+                        assert g.out[:sum(n)].isnan().all() and g.lse[:sum(n)].isnan().all()
+                        assert (g.out[sum(n):] == 7).all()
+                    with pytest.raises(lora.LoraError):  # refused twice: as once
+                        lora.lora_attend_plan_set(s.plan, kv, **dict(s.lists(), **lists))
+                    g.replay()
+                    assert g.out[:sum(n)].isnan().all()
+            s.set_plan()
+            g.check()
+        finally:
+            lora.lora_kv_destroy(wide)
+
+
+def test_a_plan_refused_before_any_was_set():
+    with Step([1], [40], [-1], [], 4, 2, 64, 16, "f16") as s:
+        with pytest.raises(lora.LoraError):
+            lora.lora_attend_plan_set(s.plan, s.kv, **dict(s.lists(), kv_len=torch.tensor([-1], dtype=torch.int32)))
+        s.check(*s.run())
+
+
+def test_a_plan_refused_during_a_capture_leaves_the_device_s():
+    """Nothing can be sent to the device then; the graph is not touched either."""
+    with Step([2], [40], [-1], [], 4, 2, 64, 16, "f16") as s:
+        s.set_plan()
+        g = Captured(s)
+        st = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        x = torch.ones(4, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(st), torch.cuda.graph(graph, stream=st):
+            y = x + 1
+            for kv in (s.kv, None):
+                with pytest.raises(lora.LoraError):
+                    lora.lora_attend_plan_set(s.plan, kv, **s.lists())
+        graph.replay()
+        torch.cuda.synchronize()
+        assert (y == 2).all()
+        g.check()

@@ -92,19 +92,6 @@ __device__ __forceinline__ float sum_over_g(float v) {
     return over_g(v, [](float x, float y) { return x + y; });
 }
 
-// The largest of a value over lanes 16 g .. 16 g + 15 (a row of lanes rotated
-// by 8, 4, 2 and 1).
-__device__ __forceinline__ uint32_t max_over_r(uint32_t v) {
-    auto turned = [](uint32_t x, auto by) {
-        return static_cast<uint32_t>(
-            __builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x120 + decltype(by)::value, 0xf, 0xf, false));
-    };
-    v = max(v, turned(v, std::integral_constant<int, 8>()));
-    v = max(v, turned(v, std::integral_constant<int, 4>()));
-    v = max(v, turned(v, std::integral_constant<int, 2>()));
-    return max(v, turned(v, std::integral_constant<int, 1>()));
-}
-
 // The token (of an item) of a query row: row / gq for row < 64, gq <= 32.
 __device__ __forceinline__ int token_of_row(const AttendArgs &a, int row) { return (row * a.gq_inv) >> 16; }
 
@@ -254,6 +241,9 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
         blk = blk < last_block ? blk : last_block;
         return ((static_cast<long>(page) * a.kv_heads + kvh) << a.page_shift) + ((blk * KV_BLOCK) & page_mask);
     };
+    // The key exponents of lane (r, g): of the keys whose elements it loads, or
+    // (fp16) of those whose scores it holds, the values' rows.
+    constexpr bool KEXP_LATE = DT == DT_F16;
     // Loads return in the order of their issue.  A tile's keys and exponents
     // are issued one tile ahead, after the scores of the tile before, its
     // values after that tile's second product; the pages of the tile after
@@ -272,13 +262,13 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
         else
             return *w;
     };
-    auto load_k = [&](long R) {
+    auto load_k = [&](long R, long vR) {
         const uint8_t *p = a.k + R * D + key_byte<D>(r & 3, g * 16);
 #pragma unroll
         for (int x = 0; x < 4; ++x)
 #pragma unroll
             for (int c = 0; c < NC; ++c) kw[x][c] = load16(p + key_byte<D>(4 * x, c * 64));
-        ke = *reinterpret_cast<const u32x4_t *>(a.kexp + R);
+        ke = *reinterpret_cast<const u32x4_t *>(a.kexp + (KEXP_LATE ? vR : R));
     };
     auto load_v = [&](long R) {
         const uint8_t *p = a.v + R * D + r * KV_BLOCK;
@@ -325,7 +315,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
     __builtin_amdgcn_sched_barrier(0);
     if (t < t_end) {
         const long vR = block_row(vb0, vp);
-        load_k(block_row(kb0, kp));
+        load_k(block_row(kb0, kp), vR);
         ve = *reinterpret_cast<const u32x4_t *>(a.vinv + vR);
         kp = block_page(kb0 + 4 * step);
         vp = block_page(vb0 + 4 * step);
@@ -345,29 +335,11 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
     auto tile = [&](auto more) __attribute__((always_inline)) {
         asm volatile("" ::: "memory");  // the queries are read again, not kept
         const int key0 = t * ATTEND_TILE;
-        // Scores.  bf16 holds any element times its scale; fp16 does for
-        // keys within 2^-15 of the tile's largest scale, and what is lost of
-        // the others is below 2^-24 of the largest, so the tile's scale is
-        // taken out of the conversion there.
-        uint32_t kb[4];
-        float cs = a.scale;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) kb[x] = (ke[x] >> (8 * (r & 3))) & 255u;
-        if constexpr (DT == DT_F16) {
-            uint32_t top = 1;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int key = key0 + 16 * (r >> 2) + 4 * x + (r & 3);
-                top = key < it.end && kb[x] > top ? kb[x] : top;
-            }
-            top = max_over_r(top);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int e = static_cast<int>(kb[x]) - static_cast<int>(top) + KV_EXP_BIAS;
-                kb[x] = e < 1 ? 1 : e > 254 ? 254 : e;
-            }
-            cs *= pow2(top);
-        }
+        // Scores.  bf16 holds any element times its scale, which the
+        // conversion takes along.  fp16 does not -- small keys beside a large
+        // one would lose bits, also to one that the row does not see -- so
+        // there the elements are converted as they are, which is exact, and
+        // the scale goes into the score.
         f32x4_t s[4][QB];
 #pragma unroll
         for (int x = 0; x < 4; ++x)
@@ -382,18 +354,19 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
                 for (int b = 0; b < QB; ++b) qv[b] = __builtin_bit_cast(V8, qf[(b * 2 * NC + 2 * c + h) * 64]);
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const V8 kf = widen<DT>(kw[x][c][2 * h], kw[x][c][2 * h + 1], pow2(kb[x]));
+                    const float scale = KEXP_LATE ? 1.0f : pow2((ke[x] >> (8 * (r & 3))) & 255u);
+                    const V8 kf = widen<DT>(kw[x][c][2 * h], kw[x][c][2 * h + 1], scale);
 #pragma unroll
                     for (int b = 0; b < QB; ++b) s[x][b] = Elem<DT>::mfma(kf, qv[b], s[x][b]);
                 }
             }
         __builtin_amdgcn_sched_barrier(0);
-        const u32x4_t vi4 = ve;
+        const u32x4_t vi4 = ve, ki4 = ke;
         long vR = 0;
         if constexpr (more) {
             const int kb1 = 4 * (t + step) + (r >> 2), vb1 = 4 * (t + step) + g;
             vR = block_row(vb1, vp);
-            load_k(block_row(kb1, kp));
+            load_k(block_row(kb1, kp), vR);
             ve = *reinterpret_cast<const u32x4_t *>(a.vinv + vR);
             kp = block_page(kb1 + 4 * step);
             vp = block_page(vb1 + 4 * step);
@@ -403,8 +376,9 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const float vi = static_cast<float>(byte_of(vi4, i));
+            const float c = KEXP_LATE ? a.scale * pow2(byte_of(ki4, i)) : a.scale;
 #pragma unroll
-            for (int b = 0; b < QB; ++b) s[i / 4][b][i % 4] = fmaf(s[i / 4][b][i % 4], cs, bm[b] - vi);
+            for (int b = 0; b < QB; ++b) s[i / 4][b][i % 4] = fmaf(s[i / 4][b][i % 4], c, bm[b] - vi);
         }
         if constexpr (more) {
             // A load after every six of these: in one burst the wave would

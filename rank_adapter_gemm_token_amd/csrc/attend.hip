@@ -430,17 +430,22 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
             }
         }
         // Weights, 8 keys an operand: half x holds keys 8 x .. 8 x + 7 of the lane's 16.
+        // Their sum is added to l as one: many light keys beside a heavy one
+        // are each below half a step of it.
         f16x8_t p[2][QB];
+        float sum[QB];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const float ib = pow2(byte_of(vi4, i));
 #pragma unroll
             for (int b = 0; b < QB; ++b) {
                 const float w = exp2_fast(s[i / 4][b][i % 4]);
-                l[b] = fmaf(w, ib, l[b]);
+                sum[b] = i == 0 ? w * ib : fmaf(w, ib, sum[b]);
                 p[i / 8][b][i % 8] = static_cast<_Float16>(w);
             }
         }
+#pragma unroll
+        for (int b = 0; b < QB; ++b) l[b] += sum[b];
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll

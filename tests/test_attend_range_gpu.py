@@ -1,10 +1,53 @@
 """Attention over the quantised cache where sizes are far apart, against the
 64-bit form, in test_attend_gpu's way."""
+import numpy as np
 import pytest
+import torch
 
-from test_attend_gpu import Step
+from rank_adapter_gemm_token_amd import lora
+from test_attend_gpu import DT, Step
 
 pytestmark = pytest.mark.gpu
+
+
+def light_and_heavy(dtype, per):
+    """Output and lse of 300 sequences over the same 2^19 keys: one of score 18,
+    the others 0; all values 1.  So many sequences, on the same pages, that each
+    is one wave's work."""
+    n, page, dim, kv_heads, B = 1 << 19, 1024, 64, 8, 300
+    heads, pages = kv_heads * per, n // page
+    kv = lora.lora_kv_create(pages, page, kv_heads, dim, dtype)
+    plan = lora.lora_attend_plan_create(B, 0, B, B * pages, heads, kv_heads, dim)
+    try:
+        k, v = (torch.full((n, kv_heads, dim), x, dtype=dtype, device="cuda") for x in (0.0, 1.0))
+        k[0, :, 3] = 18.0
+        lora.lora_kv_write(kv, k, v, torch.arange(n, dtype=torch.int32, device="cuda"), n)
+
+        def i32(x):
+            return torch.tensor(x, dtype=torch.int32)
+        lora.lora_attend_plan_set(plan, kv, i32([1] * B), i32([n] * B), i32([-1] * B),
+                                  torch.arange(pages, dtype=torch.int32).repeat(B),
+                                  torch.arange(B + 1, dtype=torch.int32) * pages)
+        q = torch.zeros((B, heads, dim), dtype=dtype, device="cuda")
+        q[:, :, 3] = 1.0
+        out, lse = torch.empty_like(q), torch.empty((B, heads), device="cuda")
+        lora.lora_attend(kv, plan, q, 1.0, out, lse)
+        return out.double().cpu().numpy(), lse.double().cpu().numpy()
+    finally:
+        torch.cuda.synchronize()
+        lora.lora_attend_plan_destroy(plan)
+        lora.lora_kv_destroy(kv)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("per", [1, 32])
+def test_many_light_keys_stay_in_the_sum(dtype, per):
+    """2^19 weights of e^-18 beside one of 1 are 1/128 of the sum, though each
+    alone is below fp32's half step at 1: one rounding of 2^-24 a tile of 64
+    keys (2^13 of them), beside that of the logarithm's terms."""
+    _, lse = light_and_heavy(DT[dtype], per)
+    want = 18.0 + np.log1p(((1 << 19) - 1) * np.exp(-18.0))
+    assert np.abs(lse - want).max() <= 2.0 ** -11 + 2.0 ** -14
 
 
 @pytest.mark.parametrize("heads,dim", [(2, 64), (8, 128)])

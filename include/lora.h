@@ -525,8 +525,10 @@ int lora_attend_plan_set(lora_attend_plan plan, lora_kv kv, const lora_attend_ba
  *          h / (n_heads / n_kv_heads)
  *   out    device, [tokens][n_heads][head_dim], contiguous; not q
  *   lse    device float [tokens][n_heads], log(sum(exp(scale * q k^T))), or NULL
- * Scores, maxima, sums and outputs are held in fp32; the weights are rounded
- * to fp16 (11 bits) for the product with the values, the output once.
+ * Scores, maxima, sums and outputs are held in fp32; the weights, times the
+ * power of two of their value row, are rounded to fp16 for the product with
+ * the values: 11 bits down to 2^-21 of the largest, absolute below that, and
+ * nothing below 2^-32.  The output is rounded once.
  * A plan of no tokens: nothing is enqueued, and q, out and lse are not looked
  * at, unless the stream is being captured.
  * Errors (nothing enqueued): LORA_EINVAL (no plan set, pointers, strides, scale

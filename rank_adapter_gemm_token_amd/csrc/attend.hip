@@ -4,13 +4,13 @@
 //
 // In the log2 domain, for one query row over keys t with scores s_t, value
 // exponents b_t (v_t = 2^b_t v8_t) and c = scale * log2(e), against an m near
-// max(c s_t + b_t):
+// max(c s_t + b_t) - 15:
 //     y_t = c s_t + (b_t - m),   p_t = 2^y_t
 //     O = sum p_t v8_t,    l = sum p_t 2^-b_t,   out = O / l,
 //     lse = ln 2 * (m + log2 l).
 // The value's exponent goes into the weight, so that the values' elements
-// feed the matrix instruction as they are and p_t is near or below 1 for
-// values of any size: exact enough in fp16.  m has at most 15 bits after the
+// feed the matrix instruction as they are and p_t is at most 2^15 for values
+// of any size: exact enough in fp16.  m has at most 15 bits after the
 // point, so b_t - m is exact and y_t is rounded once, where it is small.
 //
 // Both products are computed transposed, S^T = K Q^T and O^T = V^T P^T: the
@@ -43,10 +43,15 @@ typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
 constexpr float LN2 = 0.69314718055994530942f;
-// m is moved when a y passes it by this much.  With 32 rows moving costs: p
-// stays below 2^8, far inside fp16, and most tiles scale nothing.  With 16,
-// memory is the bound: the largest p is then 1, which fp16 holds exactly, and
-// a row with one key far above the others keeps all its bits.
+// The largest weight stands as high as fp16 reaches, at most at 2^TOP: a
+// weight keeps its 11 bits down to 2^-29 of the largest and counts down to
+// 2^-40, so that the many light keys of a long sequence, which are all in l,
+// are all in O too.  A row's m is moved when a y passes TOP, so that its
+// largest y stands slack() below.  With 32 rows moving costs, and most tiles
+// scale nothing (light keys then count down to 2^-32).  With 16, memory is the
+// bound: the largest p is a power of two, which fp16 holds exactly, and a row
+// with one key far above the others keeps all its bits.
+constexpr float TOP = 15.0f;
 constexpr float slack(int QB) { return QB == 1 ? 0.0f : 8.0f; }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -414,11 +419,11 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
                 // A row with no key yet, or with an infinite score, stays.
                 const float most = max_over_g(top[b]);
                 const float unit = fabsf(most) < 256.0f ? 32768.0f : 1.0f;
-                const float to = bm[b] - rintf(most * unit) * (1.0f / unit);
+                const float to = bm[b] - (rintf(most * unit) * (1.0f / unit) - (TOP - slack(QB)));
                 const bool move = most > thr[b] && fabsf(to) < INFINITY;
                 const float d = move ? bm[b] - to : 0.0f;
                 const float f = move && thr[b] > -INFINITY ? exp2_fast(-d) : 1.0f;
-                thr[b] = move ? slack(QB) : thr[b];
+                thr[b] = move ? TOP : thr[b];
                 bm[b] -= d;
                 l[b] *= f;
 #pragma unroll

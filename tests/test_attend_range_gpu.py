@@ -50,6 +50,18 @@ def test_many_light_keys_stay_in_the_sum(dtype, per):
     assert np.abs(lse - want).max() <= 2.0 ** -11 + 2.0 ** -14
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("per", [1, 32])
+def test_many_light_keys_stay_in_the_output(dtype, per):
+    """Light keys hold 1/128 of the whole, and all values are 1: the output is
+    1, to its own rounding and that of the weights (half a step of fp16, 2^-11;
+    with 32 rows the largest weight may stand at 2^7, so a light one is off by
+    up to 2^-25 of 2^7: 2^17 2^-32 for a quarter of them; 2^-16 for the rest)."""
+    out, _ = light_and_heavy(DT[dtype], per)
+    tol = torch.finfo(DT[dtype]).eps / 2 + 2.0 ** -11 + 2.0 ** -14 + 2.0 ** -16
+    assert np.abs(out - 1).max() <= tol, np.abs(out - 1).max()
+
+
 @pytest.mark.parametrize("heads,dim", [(2, 64), (8, 128)])
 @pytest.mark.parametrize("hidden", [200.0, 60000.0])
 def test_a_hidden_key_takes_no_bits(heads, dim, hidden):

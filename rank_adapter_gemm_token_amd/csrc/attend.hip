@@ -56,6 +56,20 @@ constexpr float slack(int QB) { return QB == 1 ? 0.0f : 8.0f; }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// l is scaled by 2^x in two halves: v_exp flushes below 2^-126, and between a
+// row of zeros (b = -64) and the largest of bf16 (b = 120) m moves by 184,
+// which l's 2^64 of that row makes up for.
+__device__ __forceinline__ float half_of(float x) { return exp2_fast(0.5f * x); }
+
+// Whether any of 16 value exponents is above 31 (a byte of vinv below 96: bit
+// 7 clear, and bit 6 or 5).
+__device__ __forceinline__ bool any_above_31(const u32x4_t &vinv) {
+    uint32_t high = 0x80808080u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) high &= vinv[i] | ((vinv[i] << 1) & (vinv[i] << 2));
+    return high != 0x80808080u;
+}
+
 // Eight e4m3 elements (two words) as an MFMA operand, scaled by a power of two.
 template <int DT>
 __device__ __forceinline__ typename Elem<DT>::vec8 widen(uint32_t lo, uint32_t hi, float scale) {
@@ -190,10 +204,10 @@ __device__ __forceinline__ void join_parts(const AttendArgs &a, const AttendToke
             if (j + k >= n) break;
             const float to = fmaxf(M, ml[k].x);
             const float ref = to == -INFINITY ? 0.0f : to;
-            const float f0 = exp2_fast(M - ref), f1 = exp2_fast(ml[k].x - ref);
+            const float h0 = half_of(M - ref), h1 = half_of(ml[k].x - ref);
             M = to;
-            L = L * f0 + ml[k].y * f1;
-            sum = sum * f0 + f32x4_t{lo[k].x, lo[k].y, hi[k].x, hi[k].y} * f1;
+            L = L * h0 * h0 + ml[k].y * h1 * h1;
+            sum = sum * (h0 * h0) + f32x4_t{lo[k].x, lo[k].y, hi[k].x, hi[k].y} * (h1 * h1);
         }
     }
     put_out<DT, D>(a, tk.token, head, d, sum, M, L);
@@ -224,6 +238,14 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
 #pragma unroll
         for (int h = 0; h < NH; ++h) o[h][b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
+
+    // p_t 2^-b_t is l's term as long as p_t is not flushed: while no m was made
+    // of an exponent above 31, that takes a term below 2^-38 of the largest (b
+    // = -64).  After one was (values of 10^12 and more, in bf16 alone), terms
+    // are made of 2^(y_t - b_t) = 2^(c s_t - m) by themselves, 2^40 larger, so
+    // that none that counts is flushed: one more exponential a weight.
+    constexpr bool SPREAD = DT == DT_BF16;
+    bool spread = false;
 
     // Of a tile of 64 keys, block j of 16 is keys 16 j .. 16 j + 15.  S^T is
     // computed in four products x = 0..3 whose row 4 j + i is key 16 j + 4 x
@@ -414,6 +436,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
         // The lanes of a row agree on m, so they only have to look at each
         // other's scores when it moves.
         if (__any(moves)) {
+            if constexpr (SPREAD) spread |= __any(any_above_31(vi4));
 #pragma unroll
             for (int b = 0; b < QB; ++b) {
                 // A row with no key yet, or with an infinite score, stays.
@@ -422,16 +445,27 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
                 const float to = bm[b] - (rintf(most * unit) * (1.0f / unit) - (TOP - slack(QB)));
                 const bool move = most > thr[b] && fabsf(to) < INFINITY;
                 const float d = move ? bm[b] - to : 0.0f;
-                const float f = move && thr[b] > -INFINITY ? exp2_fast(-d) : 1.0f;
+                const float h = move && thr[b] > -INFINITY ? half_of(-d) : 1.0f, f = h * h;
                 thr[b] = move ? TOP : thr[b];
                 bm[b] -= d;
-                l[b] *= f;
+                l[b] = l[b] * h * h;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) s[i / 4][b][i % 4] -= d;
 #pragma unroll
                 for (int h = 0; h < NH; ++h)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[h][b][i] *= f;
+            }
+        }
+        if (SPREAD && spread) {
+            asm volatile("");  // a branch
+#pragma unroll
+            for (int b = 0; b < QB; ++b) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    sum += exp2_fast(s[i / 4][b][i % 4] + (static_cast<float>(byte_of(vi4, i)) - KV_EXP_BIAS + 40.0f));
+                l[b] = fmaf(sum, 0x1p-40f, l[b]);
             }
         }
         // Weights, 8 keys an operand: half x holds keys 8 x .. 8 x + 7 of the lane's 16.
@@ -450,7 +484,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
             }
         }
 #pragma unroll
-        for (int b = 0; b < QB; ++b) l[b] += sum[b];
+        for (int b = 0; b < QB; ++b) l[b] = SPREAD ? fmaf(sum[b], spread ? 0.0f : 1.0f, l[b]) : l[b] + sum[b];
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -520,9 +554,9 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
         f32x4_t sum{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int w = 0; w < ATTEND_WAVES; ++w) {
-            const float f = exp2_fast(mw[w] - ref);
-            L = fmaf(f, lm[(w * ATTEND_ROWS + row) * 2 + 1], L);
-            sum += f * *reinterpret_cast<const f32x4_t *>(lo + (w * ATTEND_ROWS + row) * (D + 4) + d);
+            const float h = half_of(mw[w] - ref);
+            L = fmaf(h * lm[(w * ATTEND_ROWS + row) * 2 + 1], h, L);
+            sum += h * h * *reinterpret_cast<const f32x4_t *>(lo + (w * ATTEND_ROWS + row) * (D + 4) + d);
         }
         const int i = token_of_row(a, row);
         emit<DT, D, HERE>(a, it, toks[i].token, i, kvh * a.gq + row - i * a.gq, d, sum, M, L);

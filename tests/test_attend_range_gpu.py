@@ -77,3 +77,55 @@ def test_a_hidden_key_takes_no_bits(heads, dim, hidden):
         out, lse = s.run()
         last = {sum(s.q_len[:b + 1]) - 1 for b in range(B)}  # these see it
         s.check(out, lse, tokens=set(range(s.T)) - last)
+
+
+WIDE = [2.0 ** 60, 2.0 ** 71, 2.0 ** 80, 2.0 ** 100, 2.0 ** 120]
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim", [(2, 2, 64), (8, 1, 128), (64, 2, 64)])
+@pytest.mark.parametrize("vscale", WIDE)
+@pytest.mark.parametrize("kscale", [0.0, 1.0])
+def test_rows_of_zeros_beside_huge_ones(heads, kv_heads, dim, vscale, kscale):
+    """Their weights stay in the sum: in a tile, in another wave's tiles, in the
+    prefix beside huge own values and the other way round, before and after."""
+    with Step([1, 2, 1, 1, 1], [333, 40, 700, 90, 130], [0, 0, -1, 1, 1], [260, 70], heads, kv_heads, dim, 16, "bf16",
+              kscale=kscale, vscale=vscale / 16, spread=0.5) as s:
+        def slots(pages):
+            return [p * 16 + i for p in pages for i in range(16)]
+        s.v_in[slots(s.prefix_pages[0])] = 0       # a prefix of zeros before huge values
+        for at in (slots(s.pages[3]), slots(s.pages[4])):
+            s.v_in[at] = 0                         # zeros after a huge prefix
+        mixed = slots(s.pages[2])
+        s.v_in[mixed[::3]] = 0
+        s.v_in[mixed[:300]] = 0                    # some tiles of nothing else, first
+        s.v_in[slots(s.pages[1])[1::2]] = 0
+        s.write()
+        s.check(*s.run())
+
+
+@pytest.mark.parametrize("low,high", [(-64, 64), (-40, 100), (-70, 118)])
+def test_value_exponents_of_the_whole_range(low, high):
+    """Value rows of exponents from the least to the largest, in any order."""
+    with Step([1, 3, 1], [500, 90, 1111], [0, 0, -1], [300], 4, 2, 64, 16, "bf16", spread=0.3) as s:
+        e = torch.randint(low, high + 1, (s.v_in.shape[0], s.kv_heads, 1), generator=torch.Generator().manual_seed(3))
+        s.v_in = torch.ldexp(s.v_in.float(), e).to(s.dtype)
+        s.write()
+        s.check(*s.run())
+
+
+def test_light_huge_values_beside_heavy_small_ones():
+    """Values of 2^90 whose weight is 2^-100 to 2^-200 of the others', of 2^-20:
+    they decide the outputs or do not count, as the products say."""
+    for gap in (60.0, 80.0, 100.0, 140.0):
+        with Step([1, 2], [200, 70], [0, -1], [100], 4, 2, 64, 16, "bf16", kscale=0.05, vscale=2.0 ** -20,
+                  spread=0.3) as s:
+            q = torch.zeros_like(s.q)
+            q.copy_(s.q * 0.01)
+            q[..., 0] = 1.0
+            s.q, s.scale = q, 1.0
+            s.k_in[..., 0] = gap
+            huge = torch.arange(s.k_in.shape[0]) % 7 == 3
+            s.k_in[huge, :, 0] = 0.0
+            s.v_in[huge] = (s.v_in[huge].float() * 2.0 ** 110).to(s.dtype)
+            s.write()
+            s.check(*s.run())

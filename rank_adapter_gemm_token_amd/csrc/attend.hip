@@ -70,6 +70,10 @@ __device__ __forceinline__ bool any_above_31(const u32x4_t &vinv) {
     return high != 0x80808080u;
 }
 
+// bf16 keys are this power of two smaller as operands, the scale of their
+// scores larger.
+constexpr uint32_t KEXP_LESS = 8;
+
 // Eight e4m3 elements (two words) as an MFMA operand, scaled by a power of two.
 template <int DT>
 __device__ __forceinline__ typename Elem<DT>::vec8 widen(uint32_t lo, uint32_t hi, float scale) {
@@ -362,8 +366,9 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
     auto tile = [&](auto more) __attribute__((always_inline)) {
         asm volatile("" ::: "memory");  // the queries are read again, not kept
         const int key0 = t * ATTEND_TILE;
-        // Scores.  bf16 holds any element times its scale, which the
-        // conversion takes along.  fp16 does not -- small keys beside a large
+        // Scores.  bf16 holds any element times its scale (2^KEXP_LESS below it:
+        // the largest row's elements reach 2^128), which the conversion takes
+        // along.  fp16 does not -- small keys beside a large
         // one would lose bits, also to one that the row does not see -- so
         // there the elements are converted as they are, which is exact, and
         // the scale goes into the score.
@@ -381,7 +386,8 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
                 for (int b = 0; b < QB; ++b) qv[b] = __builtin_bit_cast(V8, qf[(b * 2 * NC + 2 * c + h) * 64]);
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const float scale = KEXP_LATE ? 1.0f : pow2((ke[x] >> (8 * (r & 3))) & 255u);
+                    const uint32_t byte = __builtin_amdgcn_ubfe(ke[x], 8 * (r & 3), 8);
+                    const float scale = KEXP_LATE ? 1.0f : pow2(byte - KEXP_LESS);
                     const V8 kf = widen<DT>(kw[x][c][2 * h], kw[x][c][2 * h + 1], scale);
 #pragma unroll
                     for (int b = 0; b < QB; ++b) s[x][b] = Elem<DT>::mfma(kf, qv[b], s[x][b]);
@@ -678,9 +684,11 @@ hipError_t run(const AttendArgs &a, int n_groups, int n_tokens, hipStream_t st) 
 
 }  // namespace
 
-hipError_t launch_attend(const AttendArgs &a, int dtype, int dim, int n_groups, int n_tokens, hipStream_t st) {
+hipError_t launch_attend(const AttendArgs &args, int dtype, int dim, int n_groups, int n_tokens, hipStream_t st) {
+    AttendArgs a = args;
     if (dtype == DT_F16)
         return dim == 128 ? run<DT_F16, 128>(a, n_groups, n_tokens, st) : run<DT_F16, 64>(a, n_groups, n_tokens, st);
+    a.scale *= static_cast<float>(1u << KEXP_LESS);
     return dim == 128 ? run<DT_BF16, 128>(a, n_groups, n_tokens, st) : run<DT_BF16, 64>(a, n_groups, n_tokens, st);
 }
 

@@ -129,3 +129,21 @@ def test_light_huge_values_beside_heavy_small_ones():
             s.v_in[huge] = (s.v_in[huge].float() * 2.0 ** 110).to(s.dtype)
             s.write()
             s.check(*s.run())
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("heads", [2, 64])
+def test_keys_and_values_of_the_type_s_largest(dtype, heads):
+    """Held, they stand for the next power of two, which the type has not.  A
+    query that is 0 there scores as if they were not; values of it come out
+    where they are not alone."""
+    most = torch.finfo(DT[dtype]).max
+    with Step([1, 2, 1], [40, 70, 200], [-1, 0, 0], [100], heads, 2, 64, 16, dtype, spread=0.3) as s:
+        s.q = s.q.contiguous()
+        s.q[..., 5] = 0
+        s.k_in[::3, :, 5] = most
+        s.k_in[1::3, :, 5] = -most
+        s.v_in[::9, :, 7] = most
+        s.v_in[1::9, :, 7] = -most
+        s.write()
+        s.check(*s.run())

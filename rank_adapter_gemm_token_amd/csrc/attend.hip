@@ -226,7 +226,10 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
     constexpr int NC = D / 64;   // 64-element parts of a key's row: 16 bytes a lane each
     constexpr int NH = D / 16;   // 16-element rows of V^T
     constexpr int ROWS = 16 * QB;
-    const int lane = threadIdx.x & 63;
+    int lane = threadIdx.x & 63;
+    // Made anew for each item: the compiler would keep, and spill, addresses
+    // made of it over all of them (8 registers; one sequence 10.2 us for 9.65).
+    asm volatile("" : "+v"(lane));
     const int r = lane & 15, g = lane >> 4;
     const bool joined = (it.flags & ATTEND_JOINED) != 0;
     const int step = joined ? ATTEND_WAVES : 1;

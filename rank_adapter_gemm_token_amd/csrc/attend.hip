@@ -22,11 +22,11 @@
 // on an item of its own.
 //
 // What bounds it.  Few rows a key: memory; 64 sequences of 4096 own tokens, 32
-// heads of 128, stream at 6.8 TB/s.  Many rows on one prefix: issue slots; a
-// tile of 64 keys and 32 rows is 476 vector instructions, 64 of them MFMA
-// (each costs 11 issue cycles beside others), about 2480 cycles, of which a
-// SIMD with two waves reaches 3250 (256 sequences on a prefix of 12288: 65 us,
-// 0.8 PFLOP/s).  32 rows fill the 256 registers that leave two waves a SIMD;
+// heads of 128, stream at 6.7 TB/s.  Many rows on one prefix: issue slots; a
+// tile of 64 keys and 32 rows is 454 vector instructions, 64 of them MFMA
+// (each costs 11 issue cycles beside others), about 2390 cycles.  256
+// sequences of one own token on a prefix of 12288 take 82 us with the join,
+// 0.63 PFLOP/s.  32 rows fill the 256 registers that leave two waves a SIMD;
 // 16 would widen every element twice as often.
 #include <atomic>
 #include <type_traits>
@@ -286,7 +286,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
     // the end read the last one again.
     //
     // Keys of few rows have no other reader: they pass the L2 by, which
-    // streams faster (64 sequences of 4096 tokens: 6.8 TB/s instead of 6.1)
+    // streams faster (64 sequences of 4096 tokens: 6.7 TB/s instead of 6.1)
     // and leaves it to the prefixes that several blocks of rows read.
     u32x4_t kw[4][NC], vw[NH], ke, ve;
     auto load16 = [&](const uint8_t *p) {

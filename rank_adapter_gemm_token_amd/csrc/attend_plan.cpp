@@ -225,7 +225,10 @@ int AttendPlanner::plan(const AttendBatch &b, const AttendGeometry &geo) {
     const double single = n_kv_heads_ * std::max(stream / SIMDS, waits / ATTEND_SLOTS);
     // How much of these a workgroup gets: what makes the launch shortest.  (A
     // fixed share, two a wave, left 320 workgroups for 256 CUs where 480 fit:
-    // 64 sequences with drafts took 52 us.)
+    // 64 sequences with drafts took 52 us.)  The longest span is cut into 64
+    // pieces at most, which is as far as the model has been compared with
+    // times: a span of over 16384 keys alone on one or two key/value heads
+    // could use more (131072 keys of one head: 24 us, 14 by the model).
     int64_t best = longest;
     double best_time = 0.0;
     for (int k = 1; longest > 0 && k <= 64; k += k < 8 ? 1 : k < 16 ? 2 : 8) {

@@ -95,9 +95,10 @@ __device__ __forceinline__ void quantise(const Words<N> &r, int byte, uint32_t (
 // 16 rows (at least MOST; the others are padding, or of another block), the
 // block's values are turned in LDS and move as words; the workgroup that owns
 // the neighbours' first place takes all of them.  The other tokens it owns
-// move four to a word or a byte at a time (4096 tokens, 32 heads: 23 us in
-// whole blocks, 25 us with 2% padding among them, 137 us scattered, where
-// every byte has a word of its own).
+// move four to a word or a byte at a time.  4096 tokens of 32 heads of 128: one
+// run 23 us (and 18 to read); with 2% padding among them 24; eight runs that
+// begin and end inside a block, with 2% padding, 30 (25); scattered, where
+// every byte has a word of its own, 147 (51).
 constexpr int MOST = 9;  // more than half: no two blocks have the same first place
 
 struct Tile {

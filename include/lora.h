@@ -502,6 +502,7 @@ int lora_attend_plan_destroy(lora_attend_plan plan);
 
 /* Plan a batch on caches of kv's geometry: the host cuts it, and the plan goes
  * to the device on `stream` (not while that is being captured: LORA_EINVAL).
+ * Waits only while the plan before the last is still on its way there.
  * Every list is checked first: lengths below 0, groups and page ids out of
  * range, fewer pages than a length needs are LORA_EINVAL, more new tokens
  * than max_tokens LORA_ETOKENS, a cache of other heads or head_dim

@@ -65,6 +65,7 @@ typedef struct lora_plan_s *lora_plan; /* opaque routing plan; owned by the libr
 typedef struct lora_loader_s *lora_loader; /* opaque host-to-slot loader; owned by the library */
 typedef struct lora_residency_s *lora_residency; /* opaque slot residency manager */
 typedef struct lora_kv_s *lora_kv;     /* opaque quantised key/value cache of one layer */
+typedef struct lora_rope_s *lora_rope; /* opaque table of the angles that positions turn keys and queries by */
 typedef struct lora_attend_plan_s *lora_attend_plan; /* opaque attention plan of one step's batch */
 typedef struct lora_verifier_s *lora_verifier; /* opaque workspace of lora_verify */
 
@@ -89,6 +90,8 @@ typedef enum { LORA_MODE_AUTO = 0, LORA_MODE_FUSED = 1, LORA_MODE_SEPARATE = 2 }
 
 #define LORA_KV_MAX_HEADS 256          /* key/value heads of a cache */
 #define LORA_KV_MAX_PAGE 1024          /* tokens of a page (a power of two, at least 16) */
+#define LORA_ROPE_MAX_POSITIONS (1 << 24) /* positions of a table of angles */
+#define LORA_ROPE_MAX_AXES 4           /* positions of one token */
 #define LORA_ATTEND_MAX_TOKENS 65536   /* sequences, groups and new tokens of a plan */
 #define LORA_ATTEND_MAX_PAGES (1 << 26) /* pages a plan's sequences and prefixes hold together */
 #define LORA_VERIFY_MAX_SEQS 65535     /* sequences of a verifier */
@@ -465,8 +468,54 @@ int lora_kv_write(lora_kv kv, const void *k, int64_t k_stride, const void *v, in
  * Errors (nothing enqueued): LORA_EINVAL, LORA_EHIP. */
 int lora_kv_read(lora_kv kv, const int32_t *slots, int n_tokens, void *k, void *v, void *stream);
 
+/* A table of angles on the current HIP device: what lora_kv_append turns keys
+ * and queries by.  Position p of axis axis[i] turns pair i of a head's elements
+ * by the angle p * freq[i]:
+ *     (x, y) -> scale * (x cos a - y sin a, x sin a + y cos a)
+ *   n_positions  1 .. LORA_ROPE_MAX_POSITIONS: 0 .. n_positions - 1
+ *   rot_dim      elements of a head that turn, its first ones: 16 .. 128, a
+ *                multiple of 16; the others are left as they are
+ *   freq         host [rot_dim / 2], finite
+ *   axis         host [rot_dim / 2], each 0 .. n_axes - 1; NULL: all 0
+ *   n_axes       positions of a token, 1 .. LORA_ROPE_MAX_AXES (a picture's
+ *                tokens have a time, a height and a width)
+ *   pairs        nonzero: pair i is elements 2 i and 2 i + 1; 0: elements i and
+ *                i + rot_dim / 2
+ *   scale        above 0, at most 1024
+ * Cosines and sines are held to 48 bits.  Bytes: 8 n_positions rot_dim.
+ * Allocates once, here, and waits for the device.
+ * Errors: LORA_EINVAL, LORA_ENOMEM, LORA_EHIP. */
+int lora_rope_create(int n_positions, int rot_dim, const double *freq, const int32_t *axis, int n_axes, int pairs,
+                     double scale, lora_rope *out);
+
+/* Waits for the device, then frees the table.  rope == NULL is a no-op. */
+int lora_rope_destroy(lora_rope rope);
+
+/* lora_kv_write of keys turned by their positions, and the same tokens'
+ * queries turned beside them.
+ *   rope       of the cache's device, rot_dim at most head_dim: else
+ *              LORA_EMISMATCH
+ *   k .. n_tokens  as for lora_kv_write.  A key row is quantised as it would be
+ *              from the turned key itself: no 16-bit form comes in between
+ *   positions  device int32 [n_axes][n_tokens]
+ *   q          device, [n_tokens][n_heads][head_dim], tokens q_stride elements
+ *              apart (a multiple of 8, at least n_heads * head_dim), or NULL
+ *              (then q_stride, n_heads and the next two are not looked at)
+ *   n_heads    1 .. LORA_KV_MAX_HEADS * 32
+ *   q_out      the turned queries, rounded once, tokens q_out_stride apart (as
+ *              q_stride); q itself with q's stride, or memory of its own
+ * A token with a position outside the table: its key and value are poisoned
+ * (see lora_kv_create) where it has a slot, its queries are NaN.  It is counted
+ * with the invalid slots, unless its slot is -1 (padding, whose queries are
+ * turned too).
+ * Errors (nothing enqueued): LORA_EINVAL, LORA_EMISMATCH, LORA_EHIP. */
+int lora_kv_append(lora_kv kv, lora_rope rope, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                   const int32_t *slots, const int32_t *positions, int n_tokens, const void *q, int64_t q_stride,
+                   int n_heads, void *q_out, int64_t q_out_stride, void *stream);
+
 /* Read and clear the count of slots that writes and reads found outside the
- * cache.  Waits for the device.  Errors: LORA_EINVAL, LORA_EHIP. */
+ * cache, and of tokens that appends found at positions outside the table.
+ * Waits for the device.  Errors: LORA_EINVAL, LORA_EHIP. */
 int lora_kv_poll_errors(lora_kv kv, uint64_t *n_invalid_slots);
 
 /* One step's batch, host memory (read before lora_attend_plan_set returns).

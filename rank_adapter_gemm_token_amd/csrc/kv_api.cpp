@@ -23,6 +23,7 @@ using lora::DeviceGuard;
 using lora::hip_fail;
 
 static_assert(LORA_VERIFY_MAX_VOCAB == lora::VERIFY_PART * lora::VERIFY_PARTS, "a lane for each part of a row");
+static_assert(LORA_ROPE_MAX_AXES == lora::ROPE_MAX_AXES, "the kernels keep the positions of so many");
 static_assert(LORA_VERIFY_MAX_DRAFTS == lora::VERIFY_MAX_DRAFTS, "a lane for each drafted token");
 
 struct lora_kv_s {
@@ -30,6 +31,12 @@ struct lora_kv_s {
     int page_size = 0;
     lora::KvCache c{};
     char *mem = nullptr;
+};
+
+struct lora_rope_s {
+    int device = 0;
+    char *mem = nullptr;
+    lora::RopeTable t{};
 };
 
 struct lora_attend_plan_s {
@@ -80,6 +87,14 @@ void free_plan(lora_attend_plan p) {
         if (p->sent[i]) (void)hipEventDestroy(p->sent[i]);
     }
     if (p->mem) (void)hipFree(p->mem);
+}
+
+// What lora_kv_write and lora_kv_append ask of their keys and values.
+bool rows_ok(const lora_kv_s *kv, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+             const int32_t *slots) {
+    const int64_t row = static_cast<int64_t>(kv->c.heads) * kv->c.dim;
+    return k != nullptr && v != nullptr && slots != nullptr && k_stride >= row && v_stride >= row && aligned(k, 16) &&
+           aligned(v, 16) && aligned(slots, 4) && k_stride % 8 == 0 && v_stride % 8 == 0;
 }
 
 // Checks and cuts a batch on the host.
@@ -152,10 +167,7 @@ int lora_kv_write(lora_kv kv, const void *k, int64_t k_stride, const void *v, in
                   int n_tokens, void *stream) {
     if (kv == nullptr || n_tokens < 0) return LORA_EINVAL;
     if (n_tokens == 0) return LORA_OK;
-    const int64_t row = static_cast<int64_t>(kv->c.heads) * kv->c.dim;
-    if (k == nullptr || v == nullptr || slots == nullptr || k_stride < row || v_stride < row) return LORA_EINVAL;
-    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4) || k_stride % 8 != 0 || v_stride % 8 != 0)
-        return LORA_EINVAL;
+    if (!rows_ok(kv, k, k_stride, v, v_stride, slots)) return LORA_EINVAL;
     DeviceGuard g(kv->device);
     HIP_TRY(g.error());
     HIP_TRY(lora::launch_kv_write(kv->c, k, k_stride, v, v_stride, slots, n_tokens, static_cast<hipStream_t>(stream)));
@@ -170,6 +182,86 @@ int lora_kv_read(lora_kv kv, const int32_t *slots, int n_tokens, void *k, void *
     DeviceGuard g(kv->device);
     HIP_TRY(g.error());
     HIP_TRY(lora::launch_kv_read(kv->c, slots, n_tokens, k, v, static_cast<hipStream_t>(stream)));
+    return LORA_OK;
+}
+
+int lora_rope_create(int n_positions, int rot_dim, const double *freq, const int32_t *axis, int n_axes, int pairs,
+                     double scale, lora_rope *out) {
+    if (out == nullptr) return LORA_EINVAL;
+    *out = nullptr;
+    if (n_positions < 1 || n_positions > LORA_ROPE_MAX_POSITIONS || n_axes < 1 || n_axes > LORA_ROPE_MAX_AXES)
+        return LORA_EINVAL;
+    if (rot_dim < 16 || rot_dim > 128 || rot_dim % 16 != 0 || freq == nullptr) return LORA_EINVAL;
+    if (!(scale > 0.0 && scale <= 1024.0)) return LORA_EINVAL;
+    const int n = rot_dim / 2;
+    int32_t axes[64] = {};
+    for (int i = 0; i < n; ++i) {
+        if (!std::isfinite(freq[i])) return LORA_EINVAL;
+        if (axis != nullptr) axes[i] = axis[i];
+        if (axes[i] < 0 || axes[i] >= n_axes) return LORA_EINVAL;
+    }
+    lora_rope r = new (std::nothrow) lora_rope_s;
+    if (r == nullptr) return LORA_ENOMEM;
+    const size_t half = align_up(static_cast<size_t>(n_positions) * n * sizeof(float2), 256);
+    const size_t total = 2 * half + 64 * sizeof(int32_t) + 64 * sizeof(double);
+    hipError_t e = hipGetDevice(&r->device);
+    if (e == hipSuccess) e = hipMalloc(reinterpret_cast<void **>(&r->mem), total);
+    if (e != hipSuccess) {
+        const int rc = alloc_status(e);
+        delete r;
+        return rc;
+    }
+    float2 *hi = reinterpret_cast<float2 *>(r->mem), *lo = reinterpret_cast<float2 *>(r->mem + half);
+    int32_t *axis_dev = reinterpret_cast<int32_t *>(r->mem + 2 * half);
+    double *freq_dev = reinterpret_cast<double *>(r->mem + 2 * half + 64 * sizeof(int32_t));
+    e = hipMemcpy(axis_dev, axes, static_cast<size_t>(n) * sizeof(int32_t), hipMemcpyHostToDevice);
+    if (e == hipSuccess) e = hipMemcpy(freq_dev, freq, static_cast<size_t>(n) * sizeof(double), hipMemcpyHostToDevice);
+    if (e == hipSuccess) e = lora::launch_rope_table(freq_dev, scale, n_positions, n, hi, lo, nullptr);
+    if (e == hipSuccess) e = hipDeviceSynchronize();
+    if (e != hipSuccess) {
+        const int rc = hip_fail(e);
+        (void)hipFree(r->mem);
+        delete r;
+        return rc;
+    }
+    r->t = lora::RopeTable{hi, lo, axis_dev, n_positions, n, n_axes, pairs != 0};
+    *out = r;
+    return LORA_OK;
+}
+
+int lora_rope_destroy(lora_rope rope) {
+    if (rope == nullptr) return LORA_OK;
+    const int rc = free_on(rope->device, rope->mem);
+    delete rope;
+    return rc;
+}
+
+int lora_kv_append(lora_kv kv, lora_rope rope, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                   const int32_t *slots, const int32_t *positions, int n_tokens, const void *q, int64_t q_stride,
+                   int n_heads, void *q_out, int64_t q_out_stride, void *stream) {
+    if (kv == nullptr || rope == nullptr || n_tokens < 0) return LORA_EINVAL;
+    if (rope->device != kv->device || 2 * rope->t.n > kv->c.dim) return LORA_EMISMATCH;
+    if (n_tokens == 0) return LORA_OK;
+    if (!rows_ok(kv, k, k_stride, v, v_stride, slots)) return LORA_EINVAL;
+    if (positions == nullptr || !aligned(positions, 4)) return LORA_EINVAL;
+    lora::TurnArgs a{};
+    a.t = rope->t;
+    a.positions = positions;
+    if (q != nullptr) {
+        if (n_heads < 1 || n_heads > LORA_KV_MAX_HEADS * lora::ATTEND_MAX_GQ) return LORA_EINVAL;
+        const int64_t row = static_cast<int64_t>(n_heads) * kv->c.dim;
+        if (q_out == nullptr || !aligned(q, 16) || !aligned(q_out, 16)) return LORA_EINVAL;
+        if (q_stride < row || q_out_stride < row || q_stride % 8 != 0 || q_out_stride % 8 != 0) return LORA_EINVAL;
+        if (q == q_out && q_stride != q_out_stride) return LORA_EINVAL;
+        a.q = static_cast<const uint16_t *>(q);
+        a.q_out = static_cast<uint16_t *>(q_out);
+        a.q_stride = q_stride;
+        a.out_stride = q_out_stride;
+        a.n_heads = n_heads;
+    }
+    DeviceGuard g(kv->device);
+    HIP_TRY(g.error());
+    HIP_TRY(lora::launch_kv_append(kv->c, a, k, k_stride, v, v_stride, slots, n_tokens, static_cast<hipStream_t>(stream)));
     return LORA_OK;
 }
 

@@ -1,5 +1,5 @@
 // kv_cache.hip -- keys and values quantised into the paged cache as they are
-// written, and rows of it read back.
+// written, keys turned by their positions on the way, and rows of it read back.
 //
 // A row x of D values (one token, one head) is held as e4m3 elements e and
 // one exponent s:  s the least whole number >= KV_MIN_EXP with
@@ -9,6 +9,14 @@
 // Bound by memory for long runs (4096 tokens of 32 heads of 128: 101 MB in 23
 // us, 4.4 TB/s, and back 101 MB in 18 us, 5.6 TB/s), by the chain slot -> row
 // -> store for a decode step (64 tokens: 6 and 5 us).
+//
+// An appended key is turned first: pair i of its elements, (x, y), by the angle
+// a = position * freq_i:  x cos a - y sin a,  x sin a + y cos a.  The turned
+// key has no 16-bit form in between; it is computed in fp64 from a cosine and a
+// sine of 48 bits and brought to fp32 with the last bit odd where it is not
+// exact, so that the one rounding to e4m3 falls as it does on the turned key
+// itself.  (In fp32 some element in a million falls on the other side.)
+// Queries are turned in fp32 beside it, by workgroups of their own.
 #include "dtype.hpp"
 #include "kv_internal.hpp"
 
@@ -77,17 +85,117 @@ struct Words {
 };
 
 // Elements of a row, N of them as bytes in N / 4 words.
-template <int DT, int N>
-__device__ __forceinline__ void quantise(const Words<N> &r, int byte, uint32_t (&w)[N / 4]) {
+template <int N>
+__device__ __forceinline__ void quantise(const float (&x)[N], int byte, uint32_t (&w)[N / 4]) {
     const float inv = __uint_as_float(static_cast<uint32_t>(2 * KV_EXP_BIAS - byte) << 23);
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
-        int v = __builtin_amdgcn_cvt_pk_fp8_f32(r.template at<DT>(4 * i) * inv, r.template at<DT>(4 * i + 1) * inv, 0,
-                                                false);
-        v = __builtin_amdgcn_cvt_pk_fp8_f32(r.template at<DT>(4 * i + 2) * inv, r.template at<DT>(4 * i + 3) * inv, v,
-                                            true);
+        int v = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * i] * inv, x[4 * i + 1] * inv, 0, false);
+        v = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * i + 2] * inv, x[4 * i + 3] * inv, v, true);
         w[i] = static_cast<uint32_t>(v);
     }
+}
+
+// How the elements of a head are paired to be turned.
+enum : int { TURN_NONE = 0, TURN_HALVES = 1, TURN_PAIRS = 2 };
+
+// Tokens that a workgroup may look at: its own and the 15 after them.
+constexpr int SIGHT = 2 * TOKENS - 1;
+
+struct Positions {
+    int at[ROPE_MAX_AXES][SIGHT];
+};
+
+// The positions of tokens first .. first + SIGHT - 1, for all threads after the
+// next barrier.
+__device__ __forceinline__ void load_positions(const TurnArgs &a, int n_tokens, int first, Positions &p) {
+    const int axis = threadIdx.x / SIGHT, i = threadIdx.x % SIGHT;
+    static_assert(ROPE_MAX_AXES * SIGHT <= 256, "a thread for each");
+    if (axis < a.t.n_axes)
+        p.at[axis][i] = first + i < n_tokens ? a.positions[static_cast<long>(axis) * n_tokens + first + i] : 0;
+}
+
+// What turns lane l's N elements of a row: element i of them goes to
+// x_i c + partner_i s, with the partner's sign in s.
+template <typename T, int N, int STYLE>
+struct Angles {
+    static constexpr int M = STYLE == TURN_PAIRS ? N / 2 : N;
+    T c[M], s[M];
+    bool turns;  // the lane's elements are among those that turn
+    bool bad;    // the token's position is outside the table
+
+    static __device__ __forceinline__ T join(float hi, float lo) { return static_cast<T>(hi) + static_cast<T>(lo); }
+
+    __device__ __forceinline__ void load(const RopeTable &t, const Positions &p, int token, int l) {
+        bad = false;
+        for (int a = 0; a < t.n_axes; ++a) bad |= static_cast<unsigned>(p.at[a][token]) >= static_cast<unsigned>(t.n_positions);
+        turns = l * N < 2 * t.n;
+#pragma unroll
+        for (int j = 0; j < M; ++j) c[j] = 1, s[j] = 0;
+        if (!turns || bad) return;
+        const bool second = STYLE == TURN_HALVES && l * N >= t.n;
+        const int i0 = STYLE == TURN_PAIRS ? l * M : second ? l * N - t.n : l * N;
+        constexpr bool WIDE = sizeof(T) == 8;
+        // Two pairs a load where one position turns all of them (n is a
+        // multiple of 8 and i0 of 2).
+        if (t.n_axes == 1) {
+            const long at = static_cast<long>(p.at[0][token]) * t.n + i0;
+#pragma unroll
+            for (int j = 0; j < M; j += 2) {
+                const float4 h = *reinterpret_cast<const float4 *>(t.hi + at + j);
+                float4 e{};
+                if constexpr (WIDE) e = *reinterpret_cast<const float4 *>(t.lo + at + j);
+                c[j] = join(h.x, e.x), s[j] = join(h.y, e.y);
+                c[j + 1] = join(h.z, e.z), s[j + 1] = join(h.w, e.w);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < M; ++j) {
+                const long at = static_cast<long>(p.at[t.axis[i0 + j]][token]) * t.n + i0 + j;
+                const float2 h = t.hi[at];
+                float2 e{};
+                if constexpr (WIDE) e = t.lo[at];
+                c[j] = join(h.x, e.x), s[j] = join(h.y, e.y);
+            }
+        }
+        if (STYLE == TURN_HALVES && !second)
+#pragma unroll
+            for (int j = 0; j < M; ++j) s[j] = -s[j];
+    }
+};
+
+// The words of the row that hold the partners of lane l's elements (halves:
+// another lane's of the same 16; pairs: its own).
+template <int N, int STYLE>
+__device__ __forceinline__ Words<N> partners(const Words<N> &x, int n, int l) {
+    if constexpr (STYLE == TURN_PAIRS) return x;
+    const int away = n / N, lane = threadIdx.x & 63;
+    const int from = l * N >= 2 * n ? lane : l * N < n ? lane + away : lane - away;
+    Words<N> y;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) y.w[i] = __shfl(x.w[i], from);
+    return y;
+}
+
+// fp64 to fp32, to the neighbour with the odd last bit where it is not exact:
+// any later rounding to two bits fewer falls as that of d itself would.
+__device__ __forceinline__ float to_odd(double d) {
+    const float f = static_cast<float>(d);
+    const double back = static_cast<double>(f);
+    uint32_t u = __float_as_uint(f);
+    if (back != d && fabsf(f) < INFINITY) u = (u - (fabs(back) > fabs(d) ? 1u : 0u)) | 1u;
+    return __uint_as_float(u);
+}
+
+// Element i of a row's N, turned.
+template <int DT, typename T, int N, int STYLE>
+__device__ __forceinline__ T turned(const Words<N> &x, const Words<N> &y, const Angles<T, N, STYLE> &a, int i) {
+    const T own = static_cast<T>(x.template at<DT>(i));
+    if constexpr (STYLE == TURN_PAIRS) {
+        const T other = static_cast<T>(y.template at<DT>(i ^ 1)) * a.s[i / 2];
+        return fma(own, a.c[i / 2], (i & 1) ? other : -other);
+    }
+    return fma(own, a.c[i], static_cast<T>(y.template at<DT>(i)) * a.s[i]);
 }
 
 // The tokens a workgroup deals with.  It owns 16 neighbouring tokens of the
@@ -164,20 +272,28 @@ __device__ __forceinline__ long row_of(const KvCache &c, int slot, int head) {
 
 // Workgroup: one tile of tokens and `per` neighbouring heads, one after the
 // other, the next head's rows asked for before this one's are turned.
-template <int DT, int D>
-__global__ __launch_bounds__(256) void k_kv_write(KvCache c, const uint16_t *k, int64_t k_stride, const uint16_t *v,
-                                                  int64_t v_stride, const int32_t *slots, int n_tokens, int per,
-                                                  int groups) {
+template <int DT, int D, int STYLE>
+__device__ __forceinline__ void write_tile(const KvCache &c, const TurnArgs &turn, const uint16_t *k, int64_t k_stride,
+                                           const uint16_t *v, int64_t v_stride, const int32_t *slots, int n_tokens,
+                                           int per, int groups) {
     constexpr int N = D / LANES;
     __shared__ Window w;
-    __shared__ __align__(16) uint8_t turned[2][D * VT_LD];
+    __shared__ Positions pos;
+    __shared__ __align__(16) uint8_t by_element[2][D * VT_LD];
     const int first = static_cast<int>(blockIdx.x) / groups * TOKENS, h0 = static_cast<int>(blockIdx.x) % groups * per;
     const int h1 = h0 + per < c.heads ? h0 + per : c.heads;
     const int me = threadIdx.x / LANES, l = threadIdx.x % LANES;
+    if constexpr (STYLE != TURN_NONE) load_positions(turn, n_tokens, first, pos);
     const Tile tile = find_tile(slots, n_tokens, first, c.n_pages << c.page_shift, w);
+    Angles<double, N, STYLE> angles;
+    auto look_up = [&](int i) {
+        if constexpr (STYLE != TURN_NONE) angles.load(turn.t, pos, i, l);
+    };
+    if (tile.single || h0 == 0) look_up(me);
     if (h0 == 0 && l == 0) {
         const int mine = w.s[15 + me];
-        if (first + me < n_tokens && mine != -1 && tile.slot < 0) atomicAdd(c.err, 1ull);
+        if (first + me < n_tokens && mine != -1 && (tile.slot < 0 || (STYLE != TURN_NONE && angles.bad)))
+            atomicAdd(c.err, 1ull);
     }
 
     // One row's share of a lane: its key's and value's elements.
@@ -192,24 +308,34 @@ __global__ __launch_bounds__(256) void k_kv_write(KvCache c, const uint16_t *k, 
     };
     // Writes the key and both exponents, leaves the value's bytes in vw.
     auto put = [&](const Pair &x, long R, uint32_t (&vw)[N / 4]) {
-        float ka = 0.0f, va = 0.0f;
+        float kx[N], vx[N], ka = 0.0f, va = 0.0f;
         bool fin = true;
+        if constexpr (STYLE != TURN_NONE) {
+            const Words<N> y = partners<N, STYLE>(x.k, turn.t.n, l);
+#pragma unroll
+            for (int i = 0; i < N; ++i) kx[i] = to_odd(turned<DT>(x.k, y, angles, i));
+            fin = !angles.bad;
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) kx[i] = x.k.template at<DT>(i);
+        }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const float kx = x.k.template at<DT>(i), vx = x.v.template at<DT>(i);
-            // A value that is not finite has the exponent bits all set; fmax drops NaN.
-            fin &= (__float_as_uint(kx) & 0x7F800000u) != 0x7F800000u;
-            fin &= (__float_as_uint(vx) & 0x7F800000u) != 0x7F800000u;
-            ka = fmaxf(ka, fabsf(kx));
-            va = fmaxf(va, fabsf(vx));
+            vx[i] = x.v.template at<DT>(i);
+            // A value that is not finite has the exponent bits all set (and
+            // turns into one that is not); fmax drops NaN.
+            fin &= (__float_as_uint(kx[i]) & 0x7F800000u) != 0x7F800000u;
+            fin &= (__float_as_uint(vx[i]) & 0x7F800000u) != 0x7F800000u;
+            ka = fmaxf(ka, fabsf(kx[i]));
+            va = fmaxf(va, fabsf(vx[i]));
         }
         ka = max16(ka);
         va = max16(va);
         const bool poison = max16(fin ? 0.0f : 1.0f) != 0.0f;
         const int kb = poison ? KV_EXP_BIAS : exp_byte(ka), vb = poison ? KV_EXP_BIAS : exp_byte(va);
         uint32_t kw[N / 4];
-        quantise<DT, N>(x.k, kb, kw);
-        quantise<DT, N>(x.v, vb, vw);
+        quantise<N>(kx, kb, kw);
+        quantise<N>(vx, vb, vw);
         if (poison) {
 #pragma unroll
             for (int i = 0; i < N / 4; ++i) kw[i] = 0x7F7F7F7Fu, vw[i] = 0u;
@@ -233,7 +359,7 @@ __global__ __launch_bounds__(256) void k_kv_write(KvCache c, const uint16_t *k, 
         if (tile.single) x = load(first + me, h0);
         for (int head = h0; head < h1; ++head) {
             Pair next{};
-            uint8_t *turn = turned[(head - h0) & 1];
+            uint8_t *by = by_element[(head - h0) & 1];
             uint32_t vw[N / 4] = {};
             long R = 0;
             if (tile.single) {
@@ -244,7 +370,7 @@ __global__ __launch_bounds__(256) void k_kv_write(KvCache c, const uint16_t *k, 
             if (word) {
 #pragma unroll
                 for (int i = 0; i < N; ++i)
-                    turn[(l * N + i) * VT_LD + me] = static_cast<uint8_t>(vw[i / 4] >> (8 * (i % 4)));
+                    by[(l * N + i) * VT_LD + me] = static_cast<uint8_t>(vw[i / 4] >> (8 * (i % 4)));
             }
             if (tile.any_word) __syncthreads();
             uint8_t *vd = c.v + (R & ~15L) * D + (R & 15);
@@ -253,7 +379,7 @@ __global__ __launch_bounds__(256) void k_kv_write(KvCache c, const uint16_t *k, 
                 for (int i = 0; i < N / 4; ++i) {
                     const int d = l * N + q * (N / 4) + i;
                     uint32_t four;
-                    __builtin_memcpy(&four, turn + d * VT_LD + w0, 4);
+                    __builtin_memcpy(&four, by + d * VT_LD + w0, 4);
                     *reinterpret_cast<uint32_t *>(vd - q + d * KV_BLOCK) = four;
                 }
             } else if (tile.single) {
@@ -263,7 +389,7 @@ __global__ __launch_bounds__(256) void k_kv_write(KvCache c, const uint16_t *k, 
             }
             x = next;
         }
-        if (tile.any_word) __syncthreads();  // `turned` is written again
+        if (tile.any_word) __syncthreads();  // `by_element` is written again
     }
     for (int leads = tile.leads; leads != 0; leads &= leads - 1) {
         const int place = __builtin_ctz(leads), slot0 = w.block[place], token = first + place + me;
@@ -272,10 +398,13 @@ __global__ __launch_bounds__(256) void k_kv_write(KvCache c, const uint16_t *k, 
         for (int i = 0; i < KV_BLOCK; ++i) have |= (w.s[15 + place + i] == slot0 + i) << i;
         const bool there = (have >> me) & 1;
         Pair x{};
-        if (there) x = load(token, h0);
+        if (there) {
+            x = load(token, h0);
+            look_up(place + me);
+        }
         for (int head = h0; head < h1; ++head) {
             Pair next{};
-            uint8_t *turn = turned[(head - h0) & 1];
+            uint8_t *by = by_element[(head - h0) & 1];
             uint32_t vw[N / 4] = {};
             const long R = row_of(c, slot0, head);
             if (there) {
@@ -284,12 +413,12 @@ __global__ __launch_bounds__(256) void k_kv_write(KvCache c, const uint16_t *k, 
             }
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                turn[(l * N + i) * VT_LD + me] = static_cast<uint8_t>(vw[i / 4] >> (8 * (i % 4)));
+                by[(l * N + i) * VT_LD + me] = static_cast<uint8_t>(vw[i / 4] >> (8 * (i % 4)));
             __syncthreads();
             // 256 threads x N bytes: the block's D x 16 bytes in order.
             const int at = threadIdx.x * N, d = at / KV_BLOCK, part = at % KV_BLOCK;
             uint8_t *vd = c.v + R * D + at;
-            const uint8_t *from = turn + d * VT_LD + part;
+            const uint8_t *from = by + d * VT_LD + part;
 #pragma unroll
             for (int i = 0; i < N; i += 4) {
                 const int four = (have >> (part + i)) & 15;
@@ -303,7 +432,82 @@ __global__ __launch_bounds__(256) void k_kv_write(KvCache c, const uint16_t *k, 
             }
             x = next;
         }
-        __syncthreads();  // `turned` is written again
+        __syncthreads();  // `by_element` is written again
+    }
+}
+
+template <int DT, int D>
+__global__ __launch_bounds__(256, 8) void k_kv_write(KvCache c, const uint16_t *k, int64_t k_stride, const uint16_t *v,
+                                                  int64_t v_stride, const int32_t *slots, int n_tokens, int per,
+                                                  int groups) {
+    write_tile<DT, D, TURN_NONE>(c, TurnArgs{}, k, k_stride, v, v_stride, slots, n_tokens, per, groups);
+}
+
+// Workgroup b of the queries': 16 tokens and `per` neighbouring heads, QUERIES
+// rows of a lane in flight.  A row's lanes read all of it before any writes, so
+// it may be turned in place.
+constexpr int QUERIES = 4;
+
+template <int DT, int D, int STYLE>
+__device__ __forceinline__ void turn_queries(const TurnArgs &a, int n_tokens, int b, int per, int groups) {
+    constexpr int N = D / LANES;
+    __shared__ Positions pos;
+    const int first = b / groups * TOKENS, h0 = b % groups * per;
+    const int h1 = h0 + per < a.n_heads ? h0 + per : a.n_heads;
+    const int me = threadIdx.x / LANES, l = threadIdx.x % LANES, token = first + me;
+    load_positions(a, n_tokens, first, pos);
+    __syncthreads();
+    if (token >= n_tokens) return;
+    Angles<float, N, STYLE> angles;
+    angles.load(a.t, pos, me, l);
+    const uint16_t *from = a.q + token * a.q_stride + l * N;
+    uint16_t *to = a.q_out + token * a.out_stride + l * N;
+    for (int head = h0; head < h1; head += QUERIES) {
+        Words<N> x[QUERIES];
+#pragma unroll
+        for (int j = 0; j < QUERIES; ++j) x[j].load(from + static_cast<long>(head + j < h1 ? head + j : h1 - 1) * D);
+#pragma unroll
+        for (int j = 0; j < QUERIES; ++j) {
+            if (head + j >= h1) break;
+            const Words<N> y = partners<N, STYLE>(x[j], a.t.n, l);
+            Words<N> o = x[j];
+            if (angles.turns)
+#pragma unroll
+                for (int i = 0; i < N; i += 2)
+                    o.w[i / 2] = pack<DT>(turned<DT>(x[j], y, angles, i), turned<DT>(x[j], y, angles, i + 1));
+            if (angles.bad)
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) o.w[i] = Elem<DT>::qnan * 0x10001u;
+            o.store(to + static_cast<long>(head + j) * D);
+        }
+    }
+}
+
+// The first write_wgs workgroups write keys and values, the others turn queries.
+template <int DT, int D, int STYLE>
+__global__ __launch_bounds__(256) void k_kv_append(KvCache c, TurnArgs turn, const uint16_t *k, int64_t k_stride,
+                                                   const uint16_t *v, int64_t v_stride, const int32_t *slots,
+                                                   int n_tokens, int per, int groups, unsigned write_wgs, int q_per,
+                                                   int q_groups) {
+    if (blockIdx.x < write_wgs)
+        write_tile<DT, D, STYLE>(c, turn, k, k_stride, v, v_stride, slots, n_tokens, per, groups);
+    else
+        turn_queries<DT, D, STYLE>(turn, n_tokens, static_cast<int>(blockIdx.x - write_wgs), q_per, q_groups);
+}
+
+// A position's row of the table, in fp64 and cut in two.
+__global__ __launch_bounds__(256) void k_rope_table(const double *freq, double scale, int n_positions, int n,
+                                                    float2 *hi, float2 *lo) {
+    const long all = static_cast<long>(n_positions) * n;
+    for (long i = static_cast<long>(blockIdx.x) * 256 + threadIdx.x; i < all; i += static_cast<long>(gridDim.x) * 256) {
+        const long p = i / n;
+        double sn, cs;
+        sincos(static_cast<double>(p) * freq[i - p * n], &sn, &cs);
+        cs *= scale;
+        sn *= scale;
+        const float2 h{static_cast<float>(cs), static_cast<float>(sn)};
+        hi[i] = h;
+        lo[i] = float2{static_cast<float>(cs - h.x), static_cast<float>(sn - h.y)};
     }
 }
 
@@ -405,10 +609,10 @@ __global__ __launch_bounds__(256) void k_kv_read(KvCache c, const int32_t *slots
 struct Cut {
     int per, groups;
     unsigned grid;
-    Cut(const KvCache &c, int T) {
+    Cut(int heads, int T) {
         const int tiles = (T + TOKENS - 1) / TOKENS;
-        per = tiles * static_cast<long>(c.heads) >= 4 * FULL_WGS ? 4 : 1;
-        groups = (c.heads + per - 1) / per;
+        per = tiles * static_cast<long>(heads) >= 4 * FULL_WGS ? 4 : 1;
+        groups = (heads + per - 1) / per;
         grid = static_cast<unsigned>(tiles) * static_cast<unsigned>(groups);
     }
 };
@@ -416,15 +620,26 @@ struct Cut {
 template <int DT, int D>
 hipError_t write(const KvCache &c, const void *k, int64_t ks, const void *v, int64_t vs, const int32_t *slots, int T,
                  hipStream_t st) {
-    const Cut cut(c, T);
+    const Cut cut(c.heads, T);
     k_kv_write<DT, D><<<cut.grid, 256, 0, st>>>(c, static_cast<const uint16_t *>(k), ks,
                                                 static_cast<const uint16_t *>(v), vs, slots, T, cut.per, cut.groups);
     return hipGetLastError();
 }
 
 template <int DT, int D>
+hipError_t append(const KvCache &c, const TurnArgs &a, const void *k, int64_t ks, const void *v, int64_t vs,
+                  const int32_t *slots, int T, hipStream_t st) {
+    const Cut cut(c.heads, T), q(a.q == nullptr ? 1 : a.n_heads, T);
+    auto *kernel = a.t.pairs ? k_kv_append<DT, D, TURN_PAIRS> : k_kv_append<DT, D, TURN_HALVES>;
+    kernel<<<cut.grid + (a.q == nullptr ? 0 : q.grid), 256, 0, st>>>(
+        c, a, static_cast<const uint16_t *>(k), ks, static_cast<const uint16_t *>(v), vs, slots, T, cut.per, cut.groups,
+        cut.grid, q.per, q.groups);
+    return hipGetLastError();
+}
+
+template <int DT, int D>
 hipError_t read(const KvCache &c, const int32_t *slots, int T, void *k, void *v, hipStream_t st) {
-    const Cut cut(c, T);
+    const Cut cut(c.heads, T);
     k_kv_read<DT, D><<<cut.grid, 256, 0, st>>>(c, slots, T, static_cast<uint16_t *>(k), static_cast<uint16_t *>(v),
                                                cut.per, cut.groups);
     return hipGetLastError();
@@ -439,6 +654,22 @@ hipError_t launch_kv_write(const KvCache &c, const void *k, int64_t ks, const vo
                             : write<DT_F16, 64>(c, k, ks, v, vs, slots, T, st);
     return c.dim == 128 ? write<DT_BF16, 128>(c, k, ks, v, vs, slots, T, st)
                         : write<DT_BF16, 64>(c, k, ks, v, vs, slots, T, st);
+}
+
+hipError_t launch_kv_append(const KvCache &c, const TurnArgs &turn, const void *k, int64_t ks, const void *v,
+                            int64_t vs, const int32_t *slots, int T, hipStream_t st) {
+    if (c.dtype == DT_F16)
+        return c.dim == 128 ? append<DT_F16, 128>(c, turn, k, ks, v, vs, slots, T, st)
+                            : append<DT_F16, 64>(c, turn, k, ks, v, vs, slots, T, st);
+    return c.dim == 128 ? append<DT_BF16, 128>(c, turn, k, ks, v, vs, slots, T, st)
+                        : append<DT_BF16, 64>(c, turn, k, ks, v, vs, slots, T, st);
+}
+
+hipError_t launch_rope_table(const double *freq, double scale, int n_positions, int n, float2 *hi, float2 *lo,
+                             hipStream_t st) {
+    const long blocks = (static_cast<long>(n_positions) * n + 255) / 256;
+    k_rope_table<<<static_cast<unsigned>(blocks < 65536 ? blocks : 65536), 256, 0, st>>>(freq, scale, n_positions, n, hi, lo);
+    return hipGetLastError();
 }
 
 hipError_t launch_kv_read(const KvCache &c, const int32_t *slots, int T, void *k, void *v, hipStream_t st) {

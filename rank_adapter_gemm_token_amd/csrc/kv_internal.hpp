@@ -45,6 +45,31 @@ struct KvCache {
 
 hipError_t launch_kv_write(const KvCache &c, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                            const int32_t *slots, int n_tokens, hipStream_t st);
+
+// A table of angles: for position p and pair i the cosine and the sine (times
+// the table's scale) at p * n + i, each as the sum of two floats, hi and lo.
+struct RopeTable {
+    const float2 *hi, *lo;
+    const int32_t *axis;  // [n]: which of a token's positions turns pair i
+    int n_positions, n, n_axes;
+    bool pairs;           // pair i is elements 2 i and 2 i + 1, else i and i + n
+};
+constexpr int ROPE_MAX_AXES = 4;
+
+// The tokens' positions [n_axes][n_tokens] and queries (q null: none).
+struct TurnArgs {
+    RopeTable t;
+    const int32_t *positions;
+    const uint16_t *q;
+    uint16_t *q_out;
+    int64_t q_stride, out_stride;
+    int n_heads;
+};
+
+hipError_t launch_rope_table(const double *freq, double scale, int n_positions, int n, float2 *hi, float2 *lo,
+                             hipStream_t st);
+hipError_t launch_kv_append(const KvCache &c, const TurnArgs &turn, const void *k, int64_t k_stride, const void *v,
+                            int64_t v_stride, const int32_t *slots, int n_tokens, hipStream_t st);
 hipError_t launch_kv_read(const KvCache &c, const int32_t *slots, int n_tokens, void *k, void *v, hipStream_t st);
 
 struct AttendArgs {

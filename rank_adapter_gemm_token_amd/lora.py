@@ -25,6 +25,8 @@ LORA_MAX_SLOTS = 1024
 LORA_MAX_RANK = 64
 LORA_KV_MAX_HEADS = 256
 LORA_KV_MAX_PAGE = 1024
+LORA_ROPE_MAX_POSITIONS = 1 << 24
+LORA_ROPE_MAX_AXES = 4
 LORA_ATTEND_MAX_TOKENS = 65536
 LORA_ATTEND_MAX_PAGES = 1 << 26
 LORA_VERIFY_MAX_SEQS = 65535
@@ -57,7 +59,8 @@ EXPORTS = ["lora_pool_create", "lora_pool_destroy", "lora_set_tenant_quota", "lo
            "lora_loader_create", "lora_loader_destroy", "lora_load_async", "lora_load_poll", "lora_load_wait",
            "lora_residency_create", "lora_residency_destroy", "lora_residency_set_share",
            "lora_residency_acquire", "lora_residency_release", "lora_residency_stats_read",
-           "lora_kv_create", "lora_kv_destroy", "lora_kv_write", "lora_kv_read", "lora_kv_poll_errors",
+           "lora_kv_create", "lora_kv_destroy", "lora_kv_write", "lora_kv_read", "lora_rope_create",
+           "lora_rope_destroy", "lora_kv_append", "lora_kv_poll_errors",
            "lora_attend_plan_create", "lora_attend_plan_destroy", "lora_attend_plan_set", "lora_attend",
            "lora_verifier_create", "lora_verifier_destroy", "lora_verify",
            "lora_pool_stats", "lora_tenant_bytes", "lora_poll_errors", "lora_profile_enable",
@@ -130,6 +133,9 @@ _lib.lora_kv_create.argtypes = [_i, _i, _i, _i, _i, ctypes.POINTER(_vp)]
 _lib.lora_kv_destroy.argtypes = [_vp]
 _lib.lora_kv_write.argtypes = [_vp, _vp, _i64, _vp, _i64, _vp, _i, _vp]
 _lib.lora_kv_read.argtypes = [_vp, _vp, _i, _vp, _vp, _vp]
+_lib.lora_rope_create.argtypes = [_i, _i, _vp, _vp, _i, _i, ctypes.c_double, ctypes.POINTER(_vp)]
+_lib.lora_rope_destroy.argtypes = [_vp]
+_lib.lora_kv_append.argtypes = [_vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i, _vp, _i64, _i, _vp, _i64, _vp]
 _lib.lora_kv_poll_errors.argtypes = [_vp, ctypes.POINTER(ctypes.c_uint64)]
 _lib.lora_attend_plan_create.argtypes = [_i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_vp)]
 _lib.lora_attend_plan_destroy.argtypes = [_vp]
@@ -419,9 +425,10 @@ def lora_residency_stats_read(res):
     return {name: getattr(st, name) for name, _ in lora_residency_stats._fields_}
 
 
-# Caches (heads, head_dim, dtype) and attention plans (heads, head_dim, tokens
-# of the planned batch) created through this binding.
+# Caches (heads, head_dim, dtype), tables of angles (axes) and attention plans
+# (heads, head_dim, tokens of the planned batch) created through this binding.
 _kvs = {}
+_ropes = {}
 _attend_plans = {}
 
 
@@ -480,6 +487,48 @@ def lora_kv_read(kv, slots, n_tokens, k, v, stream=None):
     n = n_tokens * heads * dim
     _check(_lib.lora_kv_read(kv, _flat(slots, n_tokens, torch.int32, "slots"), n_tokens, _flat(k, n, dtype, "k"),
                              _flat(v, n, dtype, "v"), _stream(stream)), "lora_kv_read")
+
+
+def lora_rope_create(n_positions, freq, axis=None, n_axes=1, pairs=False, scale=1.0):
+    """Returns the table's handle (an int).  freq: angle of each pair of
+    elements per position, host float64 [rot_dim / 2]; axis: host int32 of as
+    many, or None (all 0)."""
+    n = freq.numel()
+    if freq.is_cuda or freq.dtype != torch.float64 or not freq.is_contiguous():
+        raise ValueError("freq: expected contiguous host float64, got %s on %s" % (freq.dtype, freq.device))
+    if axis is not None and (axis.is_cuda or axis.dtype != torch.int32 or not axis.is_contiguous() or axis.numel() != n):
+        raise ValueError("axis: expected %d contiguous host int32 elements, got %s of %s on %s"
+                         % (n, tuple(axis.shape), axis.dtype, axis.device))
+    h = _vp()
+    _check(_lib.lora_rope_create(int(n_positions), 2 * n, freq.data_ptr(), None if axis is None else axis.data_ptr(),
+                                 int(n_axes), int(bool(pairs)), float(scale), ctypes.byref(h)), "lora_rope_create")
+    _ropes[h.value] = int(n_axes)
+    return h.value
+
+
+def lora_rope_destroy(rope):
+    _check(_lib.lora_rope_destroy(rope), "lora_rope_destroy")
+    _ropes.pop(rope, None)
+
+
+def lora_kv_append(kv, rope, k, v, slots, positions, n_tokens, q=None, q_out=None, stream=None):
+    """k, v, slots as for lora_kv_write; positions: device int32 of n_axes *
+    n_tokens elements; q, q_out: [n_tokens, n_heads, head_dim], strided over
+    tokens, or None; q_out may be q."""
+    heads, dim, dtype = _kvs[kv]
+    kp, ks = _rows(k, n_tokens, heads, dim, dtype, "k")
+    vp, vs = _rows(v, n_tokens, heads, dim, dtype, "v")
+    qp = op = None
+    n_heads = qs = os_ = 0
+    if q is not None:
+        n_heads = q.shape[1] if q.dim() == 3 else 0
+        qp, qs = _rows(q, n_tokens, n_heads, dim, dtype, "q")
+        if q_out is None:
+            raise ValueError("q_out: expected a tensor for the turned queries, got none")
+        op, os_ = _rows(q_out, n_tokens, n_heads, dim, dtype, "q_out")
+    _check(_lib.lora_kv_append(kv, rope, kp, ks, vp, vs, _flat(slots, n_tokens, torch.int32, "slots"),
+                               _flat(positions, _ropes[rope] * n_tokens, torch.int32, "positions"), n_tokens, qp, qs,
+                               n_heads, op, os_, _stream(stream)), "lora_kv_append")
 
 
 def lora_kv_poll_errors(kv):

@@ -569,6 +569,20 @@ int lora_attend_plan_destroy(lora_attend_plan plan);
  * plan that was not refused. */
 int lora_attend_plan_set(lora_attend_plan plan, lora_kv kv, const lora_attend_batch *batch, void *stream);
 
+/* As lora_attend_plan_set, for new tokens that form a tree of drafts instead of
+ * a chain (or several trees): of its sequence's new tokens, one sees itself and
+ * those above it, and no others.  The prefix and the sequence's tokens before
+ * the new ones are seen as before, and a new token's key lies where its place
+ * in the batch says, whatever its depth.
+ *   parent   host int32 [new tokens], in the batch's order: the new token of the
+ *            same sequence (0 .. its own place - 1) that it follows, or -1: it
+ *            follows the sequence's tokens before the new ones
+ * A captured lora_attend may be replayed after plans of either kind.
+ * Errors: lora_attend_plan_set's; LORA_EINVAL (parent NULL where there are new
+ * tokens, or a value of it out of range); the plan is then empty as there. */
+int lora_attend_plan_set_tree(lora_attend_plan plan, lora_kv kv, const lora_attend_batch *batch,
+                              const int32_t *parent, void *stream);
+
 /* out = softmax(scale * q k^T) v for the planned batch, the values as the cache
  * holds them, each group's prefix read once for all of its query rows.
  *   kv     a cache of the planned geometry (pages, page size, heads,

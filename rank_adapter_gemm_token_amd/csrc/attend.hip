@@ -221,7 +221,8 @@ __device__ __forceinline__ void join_parts(const AttendArgs &a, const AttendToke
 // token of the item x query head of the key head.
 template <int DT, int D, int QB, bool HERE>
 __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendItem &it, const AttendToken *toks,
-                                            const int32_t *pages, int kvh, int wave, float *lds) {
+                                            const int32_t *pages, const uint32_t *nodes, int kvh, int wave,
+                                            float *lds) {
     using V8 = typename Elem<DT>::vec8;
     constexpr int NC = D / 64;   // 64-element parts of a key's row: 16 bytes a lane each
     constexpr int NH = D / 16;   // 16-element rows of V^T
@@ -324,7 +325,6 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
     u32x4_t *qf = reinterpret_cast<u32x4_t *>(lds + wave * wave_floats(D)) + lane;
     static_assert(QB * 2 * NC * 256 + ROWS <= wave_floats(D), "the queries and tokens fit the wave's part");
     u32x4_t q0[QB][2 * NC];
-    int lim[QB];  // keys the row sees
     int tok[QB], head[QB];
 #pragma unroll
     for (int b = 0; b < QB; ++b) {
@@ -332,8 +332,6 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
         const int at = i < it.n_tok ? i : 0;
         head[b] = kvh * a.gq + row - i * a.gq;
         tok[b] = toks[at].token;
-        const int l = it.limit0 + ((it.flags & ATTEND_STEP) ? at : 0);
-        lim[b] = l < it.end ? l : it.end;
     }
 #pragma unroll
     for (int b = 0; b < QB; ++b) {
@@ -344,8 +342,11 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
             for (int h = 0; h < 2; ++h)
                 q0[b][2 * c + h] = *reinterpret_cast<const u32x4_t *>(q + c * 64 + g * 16 + h * 8);
     }
-    // Below this every row sees every key.
-    const int all = it.limit0 < it.end ? it.limit0 : it.end;
+    // Below this every row sees every key: of a tree's item the sequence's
+    // tokens before the new ones.
+    const bool in_tree = (it.flags & ATTEND_TREE) != 0;
+    const int before = it.limit0 - 1 - (it.flags >> ATTEND_FIRST_SHIFT);
+    const int sure = in_tree ? before : it.limit0, all = sure < it.end ? sure : it.end;
     __builtin_amdgcn_sched_barrier(0);
     if (t < t_end) {
         const long vR = block_row(vb0, vp);
@@ -427,11 +428,40 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
         }
         if (uniform(key0 + ATTEND_TILE > all)) {
             asm volatile("");  // a branch: as selects it would cost every tile 100 instructions
+            int row = r;
+            asm volatile("" : "+v"(row));  // what is made of it is not kept over the loop
+            uint32_t hidden[QB];           // bit i: key 16 g + i of the tile
+            if (in_tree) {
+                // Lane n looks at key key0 + n, whose node is at that place of
+                // the shifted list (which reaches a tile past the nodes on both
+                // sides), for one token of the item after the other.
+                const int key = key0 + lane;
+                const uint32_t other = nodes[key - it.limit0 + 1], mine = nodes[lane < it.n_tok ? lane : 0];
 #pragma unroll
-            for (int b = 0; b < QB; ++b)
+                for (int b = 0; b < QB; ++b) hidden[b] = 0;
+                for (int n = 0; n < it.n_tok; ++n) {
+                    const uint32_t node = __builtin_amdgcn_readlane(mine, n);
+                    const unsigned long long all =
+                        __ballot(key >= before && (key >= it.limit0 + n || !attend_above(other, node)));
+                    const uint32_t half = g < 2 ? static_cast<uint32_t>(all) : static_cast<uint32_t>(all >> 32);
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (key0 + 16 * g + i >= lim[b]) s[i / 4][b][i % 4] = -INFINITY;
+                    for (int b = 0; b < QB; ++b)
+                        if (token_of_row(a, b * 16 + row) == n) hidden[b] = half >> (16 * (g & 1));
+                }
+            } else {
+#pragma unroll
+                for (int b = 0; b < QB; ++b) {
+                    const int i = token_of_row(a, b * 16 + row);
+                    const int seen = it.limit0 + ((it.flags & ATTEND_STEP) && i < it.n_tok ? i : 0);
+                    const int n = (seen < it.end ? seen : it.end) - (key0 + 16 * g);  // of the lane's keys
+                    hidden[b] = n >= 16 ? 0u : n <= 0 ? 0xFFFFu : 0xFFFFu << n;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+#pragma unroll
+                for (int b = 0; b < QB; ++b)
+                    if ((hidden[b] >> i) & 1) s[i / 4][b][i % 4] = -INFINITY;
         }
         bool moves = false;
 #pragma unroll
@@ -615,6 +645,7 @@ __global__ __launch_bounds__(256, 2) void k_attend(AttendArgs a) {
     const AttendItem *items = reinterpret_cast<const AttendItem *>(a.meta + sizeof(AttendHeader));
     const AttendToken *toks = reinterpret_cast<const AttendToken *>(a.meta + h->token_off);
     const int32_t *pages = reinterpret_cast<const int32_t *>(a.meta + h->page_off);
+    const uint32_t *nodes = reinterpret_cast<const uint32_t *>(a.meta + h->node_off);
     if (!plan_fits(a, h)) return put_nan<DT>(a, h->n_tokens, D);
     const int n = h->n_groups * a.kv_heads;
     const int wave = uniform(threadIdx.x >> 6);
@@ -622,9 +653,9 @@ __global__ __launch_bounds__(256, 2) void k_attend(AttendArgs a) {
         const int i = w / a.kv_heads, kvh = w - i * a.kv_heads;
         const AttendItem it = items[i * ATTEND_WAVES + wave];
         if (it.n_tok * a.gq > 16)
-            attend_item<DT, D, 2, HERE>(a, it, toks + it.tok0, pages + it.page0, kvh, wave, lds);
+            attend_item<DT, D, 2, HERE>(a, it, toks + it.tok0, pages + it.page0, nodes + it.tok0, kvh, wave, lds);
         else if (it.n_tok > 0)
-            attend_item<DT, D, 1, HERE>(a, it, toks + it.tok0, pages + it.page0, kvh, wave, lds);
+            attend_item<DT, D, 1, HERE>(a, it, toks + it.tok0, pages + it.page0, nodes + it.tok0, kvh, wave, lds);
     }
 }
 

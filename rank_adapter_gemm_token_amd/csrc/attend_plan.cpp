@@ -73,6 +73,10 @@ AttendPlanner::AttendPlanner(int max_seqs, int max_groups, int max_tokens, int m
     single_.reserve(static_cast<size_t>(max_spans_));
     tokens_.reserve(static_cast<size_t>(max_tokens));
     pages_.reserve(static_cast<size_t>(max_pages) + 1);
+    nodes_.reserve(static_cast<size_t>(max_tokens));
+    size_.resize(static_cast<size_t>(max_tokens));
+    next_.resize(static_cast<size_t>(max_tokens) + 1);
+    tree_.resize(static_cast<size_t>(max_seqs));
     spans_.reserve(static_cast<size_t>(max_spans_));
     seq_tok_.resize(static_cast<size_t>(max_seqs));
     seq_page_.resize(static_cast<size_t>(max_seqs));
@@ -83,7 +87,8 @@ AttendPlanner::AttendPlanner(int max_seqs, int max_groups, int max_tokens, int m
 
 size_t AttendPlanner::max_bytes() const {
     return sizeof(AttendHeader) + static_cast<size_t>(max_groups_wg_) * ATTEND_WAVES * sizeof(AttendItem) +
-           static_cast<size_t>(max_tokens_) * sizeof(AttendToken) + (static_cast<size_t>(max_pages_) + 4) * 4;
+           static_cast<size_t>(max_tokens_) * sizeof(AttendToken) + (static_cast<size_t>(max_pages_) + 4) * 4 +
+           (static_cast<size_t>(max_tokens_) + 2 * ATTEND_NODE_PAD) * 4;
 }
 
 void AttendPlanner::clear() {
@@ -92,6 +97,7 @@ void AttendPlanner::clear() {
     single_.clear();
     tokens_.clear();
     pages_.clear();
+    nodes_.clear();
     spans_.clear();
     part_rows_ = n_split_ = 0;
 }
@@ -132,6 +138,12 @@ int AttendPlanner::check(const AttendBatch &b, const AttendGeometry &geo) const 
         if (!row(b.prefix_pages, b.prefix_page0, i, b.prefix_len[i])) return LORA_EINVAL;
     if (tokens > max_tokens_) return LORA_ETOKENS;
     if (pages > max_pages_) return LORA_EINVAL;
+    if (b.parent != nullptr) {
+        const int32_t *parent = b.parent;
+        for (int s = 0; s < b.n_seqs; parent += b.q_len[s], ++s)
+            for (int j = 0; j < b.q_len[s]; ++j)
+                if (parent[j] < -1 || parent[j] >= j) return LORA_EINVAL;
+    }
     return LORA_OK;
 }
 
@@ -179,11 +191,38 @@ int AttendPlanner::plan(const AttendBatch &b, const AttendGeometry &geo) {
         }
     }
 
+    // The trees' nodes.  A chain sees what it sees without one.
+    std::fill(tree_.begin(), tree_.end(), 0);
+    if (b.parent != nullptr) {
+        bool any = false;
+        for (int s = 0; s < b.n_seqs; ++s) {
+            const int32_t *parent = b.parent + q_first_[s];
+            for (int j = 0; j < b.q_len[s] && !tree_[s]; ++j) tree_[s] = parent[j] != j - 1;
+            any = any || tree_[s];
+        }
+        if (any) nodes_.resize(static_cast<size_t>(total));
+        for (int s = 0; any && s < b.n_seqs; ++s) {
+            const int n = b.q_len[s];
+            const int32_t *parent = b.parent + q_first_[s];
+            std::fill_n(size_.begin(), n, 1);
+            for (int j = n - 1; j >= 0; --j)
+                if (parent[j] >= 0) size_[parent[j]] += size_[j];
+            // next_[i + 1]: the number of the next child of i; next_[0]: of the next root.
+            next_[0] = 0;
+            for (int j = 0; j < n; ++j) {
+                int32_t &pre = next_[parent[j] + 1];
+                nodes_[static_cast<size_t>(seq_tok_[s] + j)] = attend_node(pre, size_[j]);
+                next_[j + 1] = pre + 1;
+                pre += size_[j];
+            }
+        }
+    }
+
     // Spans, and the tokens that none reaches (nothing to attend to).
     int64_t weight = 0;
-    auto add_span = [&](int tok0, int n, int page0, int end, int limit0, int step, bool own, int readers) {
+    auto add_span = [&](int tok0, int n, int page0, int end, int limit0, int flags, bool own, int readers) {
         const int tiles = ceil_div(end, ATTEND_TILE), c = tile_cost(n * gq, readers);
-        spans_.push_back(Span{tok0, n, page0, end, limit0, step, own, 0, tiles, static_cast<int64_t>(tiles) * c});
+        spans_.push_back(Span{tok0, n, page0, end, limit0, flags, own, 0, tiles, static_cast<int64_t>(tiles) * c});
         weight += static_cast<int64_t>(tiles) * tile_weight(n * gq);
     };
     for (int i = 0; i < b.n_groups; ++i) {
@@ -201,7 +240,8 @@ int AttendPlanner::plan(const AttendBatch &b, const AttendGeometry &geo) {
             const bool prefix = b.group[s] >= 0 && b.prefix_len[b.group[s]] > 0;
             // A block that sees nothing still has its rows to write.
             if (end > 0 || !prefix)
-                add_span(seq_tok_[s] + t, n, seq_page_[s], std::max(0, end), before + t + 1, 1, true,
+                add_span(seq_tok_[s] + t, n, seq_page_[s], std::max(0, end), before + t + 1,
+                         ATTEND_STEP | (tree_[s] ? ATTEND_TREE : 0) | t << ATTEND_FIRST_SHIFT, true,
                          ceil_div(b.q_len[s], block));
         }
     }
@@ -266,7 +306,7 @@ int AttendPlanner::plan(const AttendBatch &b, const AttendGeometry &geo) {
             const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (k + 1) / splits);
             (s.splits > 0 ? whole_ : single_)
                 .push_back(Piece{{s.tok0, s.n_tok, s.page0, t0 * ATTEND_TILE, std::min(s.end, t1 * ATTEND_TILE), s.limit0,
-                                  (s.step ? ATTEND_STEP : 0) | (s.splits > 0 ? ATTEND_JOINED : 0),
+                                  s.flags | (s.splits > 0 ? ATTEND_JOINED : 0),
                                   alone ? -1 : base + k * s.n_tok},
                                  s.cost / splits});
         }
@@ -328,11 +368,20 @@ size_t AttendPlanner::write(void *to) const {
     h.token_off = static_cast<int32_t>(sizeof h + items);
     h.page_off = static_cast<int32_t>(sizeof h + items + toks);
     char *p = static_cast<char *>(to);
+    size_t end = static_cast<size_t>(h.page_off) + pages_.size() * 4;
+    if (!nodes_.empty()) {
+        h.node_off = static_cast<int32_t>(end) + ATTEND_NODE_PAD * 4;
+        std::memset(p + end, 0, ATTEND_NODE_PAD * 4);
+        std::memcpy(p + h.node_off, nodes_.data(), nodes_.size() * 4);
+        end = static_cast<size_t>(h.node_off) + nodes_.size() * 4;
+        std::memset(p + end, 0, ATTEND_NODE_PAD * 4);
+        end += ATTEND_NODE_PAD * 4;
+    }
     std::memcpy(p, &h, sizeof h);
     if (items) std::memcpy(p + sizeof h, items_.data(), items);
     if (toks) std::memcpy(p + h.token_off, tokens_.data(), toks);
     if (!pages_.empty()) std::memcpy(p + h.page_off, pages_.data(), pages_.size() * 4);
-    return static_cast<size_t>(h.page_off) + pages_.size() * 4;
+    return end;
 }
 
 size_t AttendPlanner::write_none(void *to, int n_tokens) {

@@ -98,14 +98,45 @@ bool rows_ok(const lora_kv_s *kv, const void *k, int64_t k_stride, const void *v
 }
 
 // Checks and cuts a batch on the host.
-int plan_batch(lora_attend_plan plan, lora_kv kv, const lora_attend_batch *batch) {
+int plan_batch(lora_attend_plan plan, lora_kv kv, const lora_attend_batch *batch, const int32_t *parent) {
     if (kv == nullptr || batch == nullptr) return LORA_EINVAL;
     if (kv->device != plan->device || kv->c.heads != plan->n_kv_heads || kv->c.dim != plan->head_dim)
         return LORA_EMISMATCH;
     const lora::AttendBatch b{batch->n_seqs, batch->n_groups, batch->q_len, batch->kv_len, batch->group,
                               batch->pages, batch->page0, batch->prefix_len, batch->prefix_pages,
-                              batch->prefix_page0};
+                              batch->prefix_page0, parent};
     return plan->planner.plan(b, lora::AttendGeometry{plan->n_heads, plan->n_kv_heads, kv->page_size, kv->c.n_pages});
+}
+
+// The plan of a batch, to the device.
+int set_plan(lora_attend_plan plan, lora_kv kv, const lora_attend_batch *batch, const int32_t *parent, void *stream) {
+    if (plan == nullptr) return LORA_EINVAL;
+    std::lock_guard<std::mutex> lk(plan->mu);
+    plan->set = false;  // until this batch is on its way, whatever refuses it
+    DeviceGuard g(plan->device);
+    HIP_TRY(g.error());
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    // A captured copy would send whatever the pinned buffer holds at replay.
+    hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
+    HIP_TRY(hipStreamIsCapturing(st, &cap));
+    if (cap != hipStreamCaptureStatusNone) return LORA_EINVAL;
+    const int rc = plan_batch(plan, kv, batch, parent);
+    // A refused batch leaves the device a plan for no cache, so that graphs do
+    // not attend to the one before.
+    if (rc != LORA_OK && plan->sent_tokens < 0) return rc;
+    const int i = plan->next;
+    HIP_TRY(hipEventSynchronize(plan->sent[i]));  // done at once unless two plans are still on their way
+    const size_t bytes = rc == LORA_OK ? plan->planner.write(plan->host[i])
+                                       : lora::AttendPlanner::write_none(plan->host[i], plan->sent_tokens);
+    HIP_TRY(hipMemcpyAsync(plan->mem, plan->host[i], bytes, hipMemcpyHostToDevice, st));
+    HIP_TRY(hipEventRecord(plan->sent[i], st));
+    plan->next = 1 - i;
+    if (rc != LORA_OK) return rc;
+    plan->sent_tokens = static_cast<int>(plan->planner.tokens().size());
+    plan->page_size = kv->page_size;
+    plan->n_pages = kv->c.n_pages;
+    plan->set = true;
+    return LORA_OK;
 }
 
 }  // namespace
@@ -341,33 +372,16 @@ int lora_attend_plan_destroy(lora_attend_plan plan) {
 }
 
 int lora_attend_plan_set(lora_attend_plan plan, lora_kv kv, const lora_attend_batch *batch, void *stream) {
-    if (plan == nullptr) return LORA_EINVAL;
-    std::lock_guard<std::mutex> lk(plan->mu);
-    plan->set = false;  // until this batch is on its way, whatever refuses it
-    DeviceGuard g(plan->device);
-    HIP_TRY(g.error());
-    hipStream_t st = static_cast<hipStream_t>(stream);
-    // A captured copy would send whatever the pinned buffer holds at replay.
-    hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
-    HIP_TRY(hipStreamIsCapturing(st, &cap));
-    if (cap != hipStreamCaptureStatusNone) return LORA_EINVAL;
-    const int rc = plan_batch(plan, kv, batch);
-    // A refused batch leaves the device a plan for no cache, so that graphs do
-    // not attend to the one before.
-    if (rc != LORA_OK && plan->sent_tokens < 0) return rc;
-    const int i = plan->next;
-    HIP_TRY(hipEventSynchronize(plan->sent[i]));  // done at once unless two plans are still on their way
-    const size_t bytes = rc == LORA_OK ? plan->planner.write(plan->host[i])
-                                       : lora::AttendPlanner::write_none(plan->host[i], plan->sent_tokens);
-    HIP_TRY(hipMemcpyAsync(plan->mem, plan->host[i], bytes, hipMemcpyHostToDevice, st));
-    HIP_TRY(hipEventRecord(plan->sent[i], st));
-    plan->next = 1 - i;
-    if (rc != LORA_OK) return rc;
-    plan->sent_tokens = static_cast<int>(plan->planner.tokens().size());
-    plan->page_size = kv->page_size;
-    plan->n_pages = kv->c.n_pages;
-    plan->set = true;
-    return LORA_OK;
+    return set_plan(plan, kv, batch, nullptr, stream);
+}
+
+int lora_attend_plan_set_tree(lora_attend_plan plan, lora_kv kv, const lora_attend_batch *batch,
+                              const int32_t *parent, void *stream) {
+    // Without new tokens there is no list to give.
+    bool missing = false;
+    if (parent == nullptr && batch != nullptr && batch->q_len != nullptr)
+        for (int s = 0; s < batch->n_seqs; ++s) missing = missing || batch->q_len[s] != 0;
+    return set_plan(plan, kv, missing ? nullptr : batch, parent, stream);
 }
 
 int lora_attend(lora_kv kv, lora_attend_plan plan, const void *q, int64_t q_stride, float scale, void *out,

@@ -61,7 +61,8 @@ EXPORTS = ["lora_pool_create", "lora_pool_destroy", "lora_set_tenant_quota", "lo
            "lora_residency_acquire", "lora_residency_release", "lora_residency_stats_read",
            "lora_kv_create", "lora_kv_destroy", "lora_kv_write", "lora_kv_read", "lora_rope_create",
            "lora_rope_destroy", "lora_kv_append", "lora_kv_poll_errors",
-           "lora_attend_plan_create", "lora_attend_plan_destroy", "lora_attend_plan_set", "lora_attend",
+           "lora_attend_plan_create", "lora_attend_plan_destroy", "lora_attend_plan_set",
+           "lora_attend_plan_set_tree", "lora_attend",
            "lora_verifier_create", "lora_verifier_destroy", "lora_verify",
            "lora_pool_stats", "lora_tenant_bytes", "lora_poll_errors", "lora_profile_enable",
            "lora_profile_read", "lora_strerror", "lora_last_hip_error"]
@@ -140,6 +141,7 @@ _lib.lora_kv_poll_errors.argtypes = [_vp, ctypes.POINTER(ctypes.c_uint64)]
 _lib.lora_attend_plan_create.argtypes = [_i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_vp)]
 _lib.lora_attend_plan_destroy.argtypes = [_vp]
 _lib.lora_attend_plan_set.argtypes = [_vp, _vp, ctypes.POINTER(lora_attend_batch), _vp]
+_lib.lora_attend_plan_set_tree.argtypes = [_vp, _vp, ctypes.POINTER(lora_attend_batch), _vp, _vp]
 _lib.lora_attend.argtypes = [_vp, _vp, _vp, _i64, ctypes.c_float, _vp, _vp, _vp]
 _lib.lora_verifier_create.argtypes = [_i, ctypes.POINTER(_vp)]
 _lib.lora_verifier_destroy.argtypes = [_vp]
@@ -552,32 +554,53 @@ def lora_attend_plan_destroy(plan):
     _attend_plans.pop(plan, None)
 
 
-def lora_attend_plan_set(plan, kv, q_len, kv_len, group, pages, page0, prefix_len=None, prefix_pages=None,
-                         prefix_page0=None, stream=None):
-    """The batch's lists as host int32 tensors (lora_attend_batch in lora.h)."""
-    def host(t, n, what):
-        if t is None:
-            if n > 0:
-                raise ValueError("%s: expected %d elements, got none" % (what, n))
-            return None
-        if t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < n:
-            raise ValueError("%s: expected %d contiguous host int32 elements, got %s of %s on %s"
-                             % (what, n, tuple(t.shape), t.dtype, t.device))
-        return t.data_ptr()
+def _host(t, n, what):
+    """Pointer of a contiguous host int32 tensor of at least n elements."""
+    if t is None:
+        if n > 0:
+            raise ValueError("%s: expected %d elements, got none" % (what, n))
+        return None
+    if t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < n:
+        raise ValueError("%s: expected %d contiguous host int32 elements, got %s of %s on %s"
+                         % (what, n, tuple(t.shape), t.dtype, t.device))
+    return t.data_ptr()
+
+
+def _batch(q_len, kv_len, group, pages, page0, prefix_len=None, prefix_pages=None, prefix_page0=None):
     def lists(entries, first, n, what, first_what):
         """The entries, as many as their last bound says, and the n + 1 bounds
         (a longer tensor's further ones are not looked at)."""
-        at = host(first, n + 1 if n else 0, first_what)
-        return host(entries, int(first[n]) if n else 0, what), at
+        at = _host(first, n + 1 if n else 0, first_what)
+        return _host(entries, int(first[n]) if n else 0, what), at
     n_seqs = q_len.numel()
     n_groups = 0 if prefix_len is None else prefix_len.numel()
-    b = lora_attend_batch(n_seqs, n_groups, host(q_len, n_seqs, "q_len"), host(kv_len, n_seqs, "kv_len"),
-                          host(group, n_seqs, "group"), *lists(pages, page0, n_seqs, "pages", "page0"),
-                          host(prefix_len, n_groups, "prefix_len"),
-                          *lists(prefix_pages, prefix_page0, n_groups, "prefix_pages", "prefix_page0"))
+    return lora_attend_batch(n_seqs, n_groups, _host(q_len, n_seqs, "q_len"), _host(kv_len, n_seqs, "kv_len"),
+                             _host(group, n_seqs, "group"), *lists(pages, page0, n_seqs, "pages", "page0"),
+                             _host(prefix_len, n_groups, "prefix_len"),
+                             *lists(prefix_pages, prefix_page0, n_groups, "prefix_pages", "prefix_page0"))
+
+
+def lora_attend_plan_set(plan, kv, q_len, kv_len, group, pages, page0, prefix_len=None, prefix_pages=None,
+                         prefix_page0=None, stream=None):
+    """The batch's lists as host int32 tensors (lora_attend_batch in lora.h)."""
+    b = _batch(q_len, kv_len, group, pages, page0, prefix_len, prefix_pages, prefix_page0)
     _attend_plans[plan][2] = 0
     _check(_lib.lora_attend_plan_set(plan, kv, ctypes.byref(b), _stream(stream)), "lora_attend_plan_set")
     _attend_plans[plan][2] = int(q_len.sum())
+
+
+def lora_attend_plan_set_tree(plan, kv, parent, q_len, kv_len, group, pages, page0, prefix_len=None,
+                              prefix_pages=None, prefix_page0=None, stream=None):
+    """As lora_attend_plan_set; parent: host int32, for each new token its place
+    in its sequence's tree."""
+    b = _batch(q_len, kv_len, group, pages, page0, prefix_len, prefix_pages, prefix_page0)
+    n = int(q_len.sum())
+    if parent is None:
+        raise ValueError("parent: expected %d elements, got none" % n)
+    _attend_plans[plan][2] = 0
+    _check(_lib.lora_attend_plan_set_tree(plan, kv, ctypes.byref(b), _host(parent, n, "parent"), _stream(stream)),
+           "lora_attend_plan_set_tree")
+    _attend_plans[plan][2] = n
 
 
 def lora_attend(kv, plan, q, scale, out, lse=None, stream=None):

@@ -68,6 +68,7 @@ typedef struct lora_kv_s *lora_kv;     /* opaque quantised key/value cache of on
 typedef struct lora_rope_s *lora_rope; /* opaque table of the angles that positions turn keys and queries by */
 typedef struct lora_attend_plan_s *lora_attend_plan; /* opaque attention plan of one step's batch */
 typedef struct lora_verifier_s *lora_verifier; /* opaque workspace of lora_verify */
+typedef struct lora_scorer_s *lora_scorer; /* opaque workspace of lora_logprobs */
 
 typedef enum { LORA_F32 = 0, LORA_F16 = 1, LORA_BF16 = 2 } lora_dtype;
 
@@ -96,6 +97,8 @@ typedef enum { LORA_MODE_AUTO = 0, LORA_MODE_FUSED = 1, LORA_MODE_SEPARATE = 2 }
 #define LORA_ATTEND_MAX_PAGES (1 << 26) /* pages a plan's sequences and prefixes hold together */
 #define LORA_VERIFY_MAX_SEQS 65535     /* sequences of a verifier */
 #define LORA_VERIFY_MAX_VOCAB (1 << 21)
+#define LORA_SCORE_MAX_ROWS (1 << 20)  /* rows of a scorer */
+#define LORA_SCORE_MAX_TOP 32          /* alternatives of a row */
 #define LORA_VERIFY_MAX_DRAFTS 63      /* drafted tokens of one sequence */
 
 /* Status codes. */
@@ -637,6 +640,37 @@ int lora_verifier_destroy(lora_verifier v);
 int lora_verify(lora_verifier v, const void *p_target, const void *p_draft, lora_dtype dtype, int vocab,
                 const int32_t *draft, const int32_t *row0, const float *u, int n_seqs, int n_rows,
                 int32_t *tokens, int32_t *accepted, void *stream);
+
+/* The workspace of lora_logprobs, for up to max_rows rows a call (1 ..
+ * LORA_SCORE_MAX_ROWS).  Errors: LORA_EINVAL, LORA_ENOMEM, LORA_EHIP. */
+int lora_scorer_create(int max_rows, lora_scorer *out);
+
+/* Waits for the device, then frees it.  s == NULL is a no-op. */
+int lora_scorer_destroy(lora_scorer s);
+
+/* Log probabilities under softmax(scale * logits), row by row, each logit read
+ * once.
+ *   logits    device, rows of `vocab` in dtype (any lora_dtype), `stride`
+ *             elements apart (at least vocab); vocab 1 .. LORA_VERIFY_MAX_VOCAB
+ *   tokens    device int32 [n_rows]: the token to score, or one outside the
+ *             vocabulary (-1, say): its log probability is NaN; NULL: every
+ *             row's is
+ *   scale     2^-64 .. 2^64: one over the temperature
+ *   top       alternatives a row, 0 .. LORA_SCORE_MAX_TOP, at most vocab
+ *   logprob   device float [n_rows], of the given tokens, or NULL
+ *   entropy   device float [n_rows], -sum(p log p), or NULL
+ *   top_ids, top_logprobs  device int32, float [n_rows][top]: the largest
+ *             logits, the lower index first among equals (+0 and -0 are); not
+ *             looked at where top is 0
+ * Logits of -inf have probability 0.  A row that holds NaN or +inf, or nothing
+ * above -inf, is no distribution: its results are NaN, its top_ids -1.
+ * Sums are held in fp32 against each wave's largest logit and joined in a fixed
+ * order.  Errors (nothing enqueued): LORA_EINVAL, LORA_ETOKENS (n_rows),
+ * LORA_EHIP.
+ * Calls on one scorer on different streams are ordered by the caller. */
+int lora_logprobs(lora_scorer s, const void *logits, int64_t stride, lora_dtype dtype, int vocab,
+                  const int32_t *tokens, float scale, int top, int n_rows, float *logprob, float *entropy,
+                  int32_t *top_ids, float *top_logprobs, void *stream);
 
 /* ---------------------------------------------------------- observation -- */
 

@@ -1,6 +1,6 @@
 // kv_api.cpp -- C entry points of the quantised cache, the shared-prefix
-// attention over it and the draft verification (include/lora.h): argument
-// checks, handles and their memory, launches.  As with the pools, nothing on
+// attention over it, the draft verification and the log probabilities
+// (include/lora.h): argument checks, handles and their memory, launches.  As with the pools, nothing on
 // the hot path allocates or waits.
 #include <hip/hip_runtime.h>
 
@@ -23,6 +23,8 @@ using lora::DeviceGuard;
 using lora::hip_fail;
 
 static_assert(LORA_VERIFY_MAX_VOCAB == lora::VERIFY_PART * lora::VERIFY_PARTS, "a lane for each part of a row");
+static_assert(LORA_SCORE_MAX_TOP == lora::LOGPROBS_MAX_TOP, "the kernels have room for so many");
+static_assert(LORA_VERIFY_MAX_VOCAB == 256 * 128 * lora::LOGPROBS_MAX_PARTS, "a part is 32768 logits, or the whole row");
 static_assert(LORA_ROPE_MAX_AXES == lora::ROPE_MAX_AXES, "the kernels keep the positions of so many");
 static_assert(LORA_VERIFY_MAX_DRAFTS == lora::VERIFY_MAX_DRAFTS, "a lane for each drafted token");
 
@@ -58,6 +60,15 @@ struct lora_attend_plan_s {
 
     lora_attend_plan_s(int seqs, int groups, int tokens, int pages, int heads, int kv_heads)
         : planner(seqs, groups, tokens, pages, heads, kv_heads) {}
+};
+
+struct lora_scorer_s {
+    int device = 0;
+    int max_rows = 0;
+    char *mem = nullptr;
+    uint64_t *keys = nullptr;
+    float *stats = nullptr;
+    unsigned *count = nullptr;
 };
 
 struct lora_verifier_s {
@@ -500,6 +511,74 @@ int lora_verify(lora_verifier v, const void *p_target, const void *p_draft, lora
     const int wgs = 256 / n_seqs;
     a.group = wgs < 1 ? a.parts : (a.parts + wgs - 1) / wgs;
     HIP_TRY(lora::launch_verify(a, static_cast<int>(dtype), static_cast<hipStream_t>(stream)));
+    return LORA_OK;
+}
+
+int lora_scorer_create(int max_rows, lora_scorer *out) {
+    if (out == nullptr) return LORA_EINVAL;
+    *out = nullptr;
+    if (max_rows < 1 || max_rows > LORA_SCORE_MAX_ROWS) return LORA_EINVAL;
+    lora_scorer s = new (std::nothrow) lora_scorer_s;
+    if (s == nullptr) return LORA_ENOMEM;
+    s->max_rows = max_rows;
+    const size_t keys = static_cast<size_t>(lora::LOGPROBS_WGS) * lora::LOGPROBS_MAX_TOP * sizeof(uint64_t);
+    const size_t stats = static_cast<size_t>(lora::LOGPROBS_WGS) * 4 * sizeof(float);
+    const size_t total = keys + stats + static_cast<size_t>(lora::LOGPROBS_WGS) * sizeof(unsigned);
+    hipError_t e = hipGetDevice(&s->device);
+    if (e == hipSuccess) e = hipMalloc(reinterpret_cast<void **>(&s->mem), total);
+    if (e == hipSuccess) e = hipMemset(s->mem, 0, total);
+    if (e == hipSuccess) e = hipDeviceSynchronize();
+    if (e != hipSuccess) {
+        const int rc = alloc_status(e);
+        if (s->mem) (void)hipFree(s->mem);
+        delete s;
+        return rc;
+    }
+    s->keys = reinterpret_cast<uint64_t *>(s->mem);
+    s->stats = reinterpret_cast<float *>(s->mem + keys);
+    s->count = reinterpret_cast<unsigned *>(s->mem + keys + stats);
+    *out = s;
+    return LORA_OK;
+}
+
+int lora_scorer_destroy(lora_scorer s) {
+    if (s == nullptr) return LORA_OK;
+    const int rc = free_on(s->device, s->mem);
+    delete s;
+    return rc;
+}
+
+int lora_logprobs(lora_scorer s, const void *logits, int64_t stride, lora_dtype dtype, int vocab,
+                  const int32_t *tokens, float scale, int top, int n_rows, float *logprob, float *entropy,
+                  int32_t *top_ids, float *top_logprobs, void *stream) {
+    if (s == nullptr || n_rows < 0 || vocab < 1 || vocab > LORA_VERIFY_MAX_VOCAB || stride < vocab) return LORA_EINVAL;
+    if (dtype != LORA_F32 && dtype != LORA_F16 && dtype != LORA_BF16) return LORA_EINVAL;
+    if (!(scale >= 0x1p-64f && scale <= 0x1p64f) || top < 0 || top > LORA_SCORE_MAX_TOP || top > vocab)
+        return LORA_EINVAL;
+    if (n_rows == 0) return LORA_OK;
+    if (n_rows > s->max_rows) return LORA_ETOKENS;
+    if (logits == nullptr || !aligned(logits, dtype == LORA_F32 ? 4 : 2)) return LORA_EINVAL;
+    if (top > 0 && (top_ids == nullptr || top_logprobs == nullptr)) return LORA_EINVAL;
+    if (!aligned(tokens, 4) || !aligned(logprob, 4) || !aligned(entropy, 4)) return LORA_EINVAL;
+    if (top > 0 && (!aligned(top_ids, 4) || !aligned(top_logprobs, 4))) return LORA_EINVAL;
+    DeviceGuard g(s->device);
+    HIP_TRY(g.error());
+    lora::LogprobsArgs a{};
+    a.z = logits;
+    a.stride = stride;
+    a.tokens = tokens;
+    a.c = scale * 1.44269504088896340736f;
+    a.n_rows = n_rows;
+    a.vocab = vocab;
+    a.top = top;
+    a.logprob = logprob;
+    a.entropy = entropy;
+    a.top_ids = top_ids;
+    a.top_logprobs = top_logprobs;
+    a.keys = s->keys;
+    a.stats = s->stats;
+    a.count = s->count;
+    HIP_TRY(lora::launch_logprobs(a, static_cast<int>(dtype), static_cast<hipStream_t>(stream)));
     return LORA_OK;
 }
 

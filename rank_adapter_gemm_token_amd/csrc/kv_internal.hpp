@@ -105,4 +105,26 @@ constexpr int VERIFY_MAX_DRAFTS = 63; // drafted tokens of a sequence
 
 hipError_t launch_verify(const VerifyArgs &a, int dtype, hipStream_t st);
 
+struct LogprobsArgs {
+    const void *z;
+    int64_t stride;        // logits from one row to the next
+    const int32_t *tokens; // or null
+    float c;               // scale times log2(e)
+    int n_rows, vocab, top;
+    float *logprob, *entropy;  // either null: not asked for
+    int32_t *top_ids;
+    float *top_logprobs;
+    // Of rows that several workgroups share, LOGPROBS_WGS of these at most:
+    uint64_t *keys;        // [rows][workgroups][LOGPROBS_MAX_TOP]
+    float *stats;          // [rows][workgroups][4]
+    unsigned *count;       // [rows], 0 between calls
+    // Chosen by the launch.
+    int threads, parts, group;
+};
+constexpr int LOGPROBS_MAX_TOP = 32;
+constexpr int LOGPROBS_MAX_PARTS = 64;  // parts of a row at most
+constexpr int LOGPROBS_WGS = 256;       // workgroups that rows are shared by at most
+
+hipError_t launch_logprobs(const LogprobsArgs &a, int dtype, hipStream_t st);
+
 }  // namespace lora

@@ -32,6 +32,8 @@ LORA_ATTEND_MAX_PAGES = 1 << 26
 LORA_VERIFY_MAX_SEQS = 65535
 LORA_VERIFY_MAX_VOCAB = 1 << 21
 LORA_VERIFY_MAX_DRAFTS = 63
+LORA_SCORE_MAX_ROWS = 1 << 20
+LORA_SCORE_MAX_TOP = 32
 
 LORA_OK = 0
 LORA_EINVAL = -1
@@ -64,6 +66,7 @@ EXPORTS = ["lora_pool_create", "lora_pool_destroy", "lora_set_tenant_quota", "lo
            "lora_attend_plan_create", "lora_attend_plan_destroy", "lora_attend_plan_set",
            "lora_attend_plan_set_tree", "lora_attend",
            "lora_verifier_create", "lora_verifier_destroy", "lora_verify",
+           "lora_scorer_create", "lora_scorer_destroy", "lora_logprobs",
            "lora_pool_stats", "lora_tenant_bytes", "lora_poll_errors", "lora_profile_enable",
            "lora_profile_read", "lora_strerror", "lora_last_hip_error"]
 
@@ -146,6 +149,9 @@ _lib.lora_attend.argtypes = [_vp, _vp, _vp, _i64, ctypes.c_float, _vp, _vp, _vp]
 _lib.lora_verifier_create.argtypes = [_i, ctypes.POINTER(_vp)]
 _lib.lora_verifier_destroy.argtypes = [_vp]
 _lib.lora_verify.argtypes = [_vp, _vp, _vp, _i, _i, _vp, _vp, _vp, _i, _i, _vp, _vp, _vp]
+_lib.lora_scorer_create.argtypes = [_i, ctypes.POINTER(_vp)]
+_lib.lora_scorer_destroy.argtypes = [_vp]
+_lib.lora_logprobs.argtypes = [_vp, _vp, _i64, _i, _i, _vp, ctypes.c_float, _i, _i, _vp, _vp, _vp, _vp, _vp]
 _lib.lora_pool_stats.argtypes = [_vp, ctypes.POINTER(lora_stats)]
 _lib.lora_tenant_bytes.argtypes = [_vp, ctypes.c_int32, ctypes.POINTER(ctypes.c_uint64)]
 _lib.lora_poll_errors.argtypes = [_vp, ctypes.POINTER(ctypes.c_uint64)]
@@ -637,6 +643,46 @@ def lora_verify(verifier, p_target, p_draft, draft, row0, u, n_seqs, n_rows, tok
                             _flat(u, n_rows, torch.float32, "u"), n_seqs, n_rows,
                             _flat(tokens, n_rows, i32, "tokens"), _flat(accepted, n_seqs, i32, "accepted"),
                             _stream(stream)), "lora_verify")
+
+
+def lora_scorer_create(max_rows):
+    """Returns the scorer handle (an int)."""
+    h = _vp()
+    _check(_lib.lora_scorer_create(int(max_rows), ctypes.byref(h)), "lora_scorer_create")
+    return h.value
+
+
+def lora_scorer_destroy(scorer):
+    _check(_lib.lora_scorer_destroy(scorer), "lora_scorer_destroy")
+
+
+def lora_logprobs(scorer, logits, tokens, scale=1.0, logprob=None, entropy=None, top_ids=None, top_logprobs=None,
+                  stream=None):
+    """logits: [n_rows, vocab], strided over rows; tokens: device int32 or None;
+    logprob, entropy: device float32 of n_rows elements or None; top_ids,
+    top_logprobs: device int32 and float32 [n_rows, top], or None (top is 0)."""
+    if logits.dim() != 2 or not logits.is_cuda or logits.dtype not in DTYPE_OF:
+        raise ValueError("logits: expected a device tensor [rows, vocab], got %s of %s on %s"
+                         % (tuple(logits.shape), logits.dtype, logits.device))
+    n, vocab = logits.shape
+    stride = logits.stride(0) if n > 1 else vocab  # a single row's stride says nothing
+    if vocab > 1 and logits.stride(1) != 1:
+        raise ValueError("logits: a row must be contiguous, got strides %s" % (logits.stride(),))
+    if (top_ids is None) != (top_logprobs is None):
+        raise ValueError("top_ids, top_logprobs: expected both or neither")
+    top = 0
+    if top_ids is not None:
+        if top_ids.dim() != 2 or top_ids.shape[0] != n:
+            raise ValueError("top_ids: expected [%d, top], got %s" % (n, tuple(top_ids.shape)))
+        top = top_ids.shape[1]
+    f32, i32 = torch.float32, torch.int32
+    _check(_lib.lora_logprobs(scorer, logits.data_ptr(), stride, DTYPE_OF[logits.dtype], vocab,
+                              None if tokens is None else _flat(tokens, n, i32, "tokens"), scale, top, n,
+                              None if logprob is None else _flat(logprob, n, f32, "logprob"),
+                              None if entropy is None else _flat(entropy, n, f32, "entropy"),
+                              _flat(top_ids, n * top, i32, "top_ids") if top else None,
+                              _flat(top_logprobs, n * top, f32, "top_logprobs") if top else None, _stream(stream)),
+           "lora_logprobs")
 
 
 def lora_pool_stats(pool):

@@ -43,14 +43,12 @@ def logprobs(z, token, scale, k):
     that holds NaN or +inf, or nothing above -inf, is no distribution."""
     if np.isnan(z).any() or not math.isfinite(z.max()):
         return math.nan, math.nan, [-1] * k, [math.nan] * k
-    y = z * scale
-    m = y.max()
-    e = np.exp(y - m)
-    lse = m + math.log(math.fsum(e))
-    lp = y - lse
+    y = (z - z.max()) * scale  # before the sum: far from 0 a logarithm would be lost beside the logit
+    e = np.exp(y)
+    lp = y - math.log(math.fsum(e))
     some = e > 0
     entropy = -math.fsum(np.exp(lp[some]) * lp[some])
-    ids = sorted(range(len(z)), key=lambda i: (-z[i], i))[:k]
+    ids = np.argsort(-z, kind="stable")[:k].tolist()  # the lower index first among equals
     return (lp[token] if 0 <= token < len(z) else math.nan), entropy, ids, [lp[i] for i in ids]
 
 

@@ -135,13 +135,14 @@ __global__ __launch_bounds__(THREADS) void k_verify(VerifyArgs a) {
     __shared__ unsigned arrived;
 
     const int r0 = a.row0[b], r1 = a.row0[b + 1];
-    const int n = r1 - r0 - 1;
     // Every sequence has a row at least: b rows come before, n_seqs - 1 - b
-    // after.  A list that says otherwise is not followed.
-    if (r0 < b || n < 0 || n > VERIFY_MAX_DRAFTS || r1 > a.n_rows - (a.n_seqs - 1 - b)) {
+    // after.  A list that says otherwise is not followed.  (The bounds are
+    // compared before their difference is made, which may pass 32 bits.)
+    if (r0 < b || r1 <= r0 || r1 > a.n_rows - (a.n_seqs - 1 - b) || r1 - r0 - 1 > VERIFY_MAX_DRAFTS) {
         if (c == 0 && t == 0) a.accepted[b] = -1;
         return;
     }
+    const int n = r1 - r0 - 1;
     // Lane i looks at drafted token i.
     const int lane = t & 63, wave = uniform(t >> 6);
     bool keep = false, bad = false;

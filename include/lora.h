@@ -67,7 +67,7 @@ typedef struct lora_residency_s *lora_residency; /* opaque slot residency manage
 typedef struct lora_kv_s *lora_kv;     /* opaque quantised key/value cache of one layer */
 typedef struct lora_rope_s *lora_rope; /* opaque table of the angles that positions turn keys and queries by */
 typedef struct lora_attend_plan_s *lora_attend_plan; /* opaque attention plan of one step's batch */
-typedef struct lora_verifier_s *lora_verifier; /* opaque workspace of lora_verify */
+typedef struct lora_verifier_s *lora_verifier; /* opaque workspace of lora_verify and lora_verify_tree */
 typedef struct lora_scorer_s *lora_scorer; /* opaque workspace of lora_logprobs */
 
 typedef enum { LORA_F32 = 0, LORA_F16 = 1, LORA_BF16 = 2 } lora_dtype;
@@ -606,7 +606,7 @@ int lora_attend_plan_set_tree(lora_attend_plan plan, lora_kv kv, const lora_atte
 int lora_attend(lora_kv kv, lora_attend_plan plan, const void *q, int64_t q_stride, float scale, void *out,
                 float *lse, void *stream);
 
-/* The workspace of lora_verify, for up to max_seqs sequences a call.
+/* The workspace of lora_verify and lora_verify_tree, for up to max_seqs sequences a call.
  * Errors: LORA_EINVAL, LORA_ENOMEM, LORA_EHIP. */
 int lora_verifier_create(int max_seqs, lora_verifier *out);
 
@@ -640,6 +640,40 @@ int lora_verifier_destroy(lora_verifier v);
 int lora_verify(lora_verifier v, const void *p_target, const void *p_draft, lora_dtype dtype, int vocab,
                 const int32_t *draft, const int32_t *row0, const float *u, int n_seqs, int n_rows,
                 int32_t *tokens, int32_t *accepted, void *stream);
+
+/* Walk down drafted trees along the target's own draws.  Sequence s has rows
+ * row0[s] .. row0[s + 1] - 1, at least one: its new tokens as
+ * lora_attend_plan_set_tree has them, the last token already known first (node
+ * 0), the drafted ones after it, and after each the target's probabilities of
+ * the next.  From node 0 on, a token is drawn from the node's row with the
+ * node's u: the first index at which the running sum, in fp64, passes u times
+ * the whole.  The first child of the node that holds it is kept and the walk
+ * goes on there; where none does, the walk ends.  So every token is distributed
+ * as the target's, however the tree was drafted.
+ *   p_target   device [n_rows][vocab], probabilities in dtype (any lora_dtype);
+ *              what is not above 0 counts as nothing
+ *   draft      device int32 [n_rows]: the tokens of the nodes (of node 0: not
+ *              looked at)
+ *   parent     device int32 [n_rows]: as lora_attend_plan_set_tree's.  A node
+ *              that is no later one's child (-1, itself, one after it) is
+ *              never come to
+ *   row0       device int32 [n_seqs + 1], strictly ascending from 0 to n_rows
+ *   u          device float [n_rows], of [0, 1)
+ *   accepted   device int32 [n_seqs]: how many drafted tokens were kept, k
+ *   tokens     device int32 [n_rows]: at row0[s] the k kept tokens, then the
+ *              last one drawn, then -1
+ *   path       device int32 [n_rows]: at row0[s] the k + 1 nodes that these
+ *              were drawn at (0 first): the places of the new tokens whose keys
+ *              and values stay; then -1
+ * accepted is -1, and the sequence's tokens and path are, where a row on the
+ * way has no weight (no entry above 0, or a sum that is not finite); also, with
+ * nothing else written, where the sequence's two entries of row0 do not ascend
+ * or leave no row for each sequence before and after it.
+ * Errors (nothing enqueued): LORA_EINVAL, LORA_ETOKENS (n_seqs), LORA_EHIP.
+ * Calls on one verifier on different streams are ordered by the caller. */
+int lora_verify_tree(lora_verifier v, const void *p_target, lora_dtype dtype, int vocab, const int32_t *draft,
+                     const int32_t *parent, const int32_t *row0, const float *u, int n_seqs, int n_rows,
+                     int32_t *tokens, int32_t *path, int32_t *accepted, void *stream);
 
 /* The workspace of lora_logprobs, for up to max_rows rows a call (1 ..
  * LORA_SCORE_MAX_ROWS).  Errors: LORA_EINVAL, LORA_ENOMEM, LORA_EHIP. */

@@ -514,6 +514,39 @@ int lora_verify(lora_verifier v, const void *p_target, const void *p_draft, lora
     return LORA_OK;
 }
 
+int lora_verify_tree(lora_verifier v, const void *p_target, lora_dtype dtype, int vocab, const int32_t *draft,
+                     const int32_t *parent, const int32_t *row0, const float *u, int n_seqs, int n_rows,
+                     int32_t *tokens, int32_t *path, int32_t *accepted, void *stream) {
+    if (v == nullptr || n_seqs < 0 || n_rows < 0 || vocab < 1 || vocab > LORA_VERIFY_MAX_VOCAB) return LORA_EINVAL;
+    if (dtype != LORA_F32 && dtype != LORA_F16 && dtype != LORA_BF16) return LORA_EINVAL;
+    if (n_seqs == 0) return LORA_OK;
+    if (n_seqs > v->max_seqs) return LORA_ETOKENS;
+    if (row0 == nullptr || accepted == nullptr || !aligned(row0, 4) || !aligned(accepted, 4)) return LORA_EINVAL;
+    if (n_rows > 0 && (p_target == nullptr || draft == nullptr || parent == nullptr || u == nullptr ||
+                       tokens == nullptr || path == nullptr))
+        return LORA_EINVAL;
+    if (!aligned(p_target, dtype == LORA_F32 ? 4 : 2) || !aligned(draft, 4) || !aligned(parent, 4) || !aligned(u, 4) ||
+        !aligned(tokens, 4) || !aligned(path, 4))
+        return LORA_EINVAL;
+    DeviceGuard g(v->device);
+    HIP_TRY(g.error());
+    lora::VerifyTreeArgs a{};
+    a.p = p_target;
+    a.draft = draft;
+    a.parent = parent;
+    a.row0 = row0;
+    a.u = u;
+    a.tokens = tokens;
+    a.path = path;
+    a.accepted = accepted;
+    a.n_seqs = n_seqs;
+    a.n_rows = n_rows;
+    a.vocab = vocab;
+    a.parts = (vocab + lora::VERIFY_PART - 1) / lora::VERIFY_PART;
+    HIP_TRY(lora::launch_verify_tree(a, static_cast<int>(dtype), static_cast<hipStream_t>(stream)));
+    return LORA_OK;
+}
+
 int lora_scorer_create(int max_rows, lora_scorer *out) {
     if (out == nullptr) return LORA_EINVAL;
     *out = nullptr;

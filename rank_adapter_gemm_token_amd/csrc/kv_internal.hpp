@@ -105,6 +105,16 @@ constexpr int VERIFY_MAX_DRAFTS = 63; // drafted tokens of a sequence
 
 hipError_t launch_verify(const VerifyArgs &a, int dtype, hipStream_t st);
 
+struct VerifyTreeArgs {
+    const void *p;
+    const int32_t *draft, *parent, *row0;
+    const float *u;
+    int32_t *tokens, *path, *accepted;
+    int n_seqs, n_rows, vocab, parts;
+};
+
+hipError_t launch_verify_tree(const VerifyTreeArgs &a, int dtype, hipStream_t st);
+
 struct LogprobsArgs {
     const void *z;
     int64_t stride;        // logits from one row to the next

@@ -66,7 +66,7 @@ EXPORTS = ["lora_pool_create", "lora_pool_destroy", "lora_set_tenant_quota", "lo
            "lora_attend_plan_create", "lora_attend_plan_destroy", "lora_attend_plan_set",
            "lora_attend_plan_set_tree", "lora_attend",
            "lora_verifier_create", "lora_verifier_destroy", "lora_verify",
-           "lora_scorer_create", "lora_scorer_destroy", "lora_logprobs",
+           "lora_verify_tree", "lora_scorer_create", "lora_scorer_destroy", "lora_logprobs",
            "lora_pool_stats", "lora_tenant_bytes", "lora_poll_errors", "lora_profile_enable",
            "lora_profile_read", "lora_strerror", "lora_last_hip_error"]
 
@@ -149,6 +149,7 @@ _lib.lora_attend.argtypes = [_vp, _vp, _vp, _i64, ctypes.c_float, _vp, _vp, _vp]
 _lib.lora_verifier_create.argtypes = [_i, ctypes.POINTER(_vp)]
 _lib.lora_verifier_destroy.argtypes = [_vp]
 _lib.lora_verify.argtypes = [_vp, _vp, _vp, _i, _i, _vp, _vp, _vp, _i, _i, _vp, _vp, _vp]
+_lib.lora_verify_tree.argtypes = [_vp, _vp, _i, _i, _vp, _vp, _vp, _vp, _i, _i, _vp, _vp, _vp, _vp]
 _lib.lora_scorer_create.argtypes = [_i, ctypes.POINTER(_vp)]
 _lib.lora_scorer_destroy.argtypes = [_vp]
 _lib.lora_logprobs.argtypes = [_vp, _vp, _i64, _i, _i, _vp, ctypes.c_float, _i, _i, _vp, _vp, _vp, _vp, _vp]
@@ -643,6 +644,17 @@ def lora_verify(verifier, p_target, p_draft, draft, row0, u, n_seqs, n_rows, tok
                             _flat(u, n_rows, torch.float32, "u"), n_seqs, n_rows,
                             _flat(tokens, n_rows, i32, "tokens"), _flat(accepted, n_seqs, i32, "accepted"),
                             _stream(stream)), "lora_verify")
+
+
+def lora_verify_tree(verifier, p_target, draft, parent, row0, u, n_seqs, n_rows, tokens, path, accepted, stream=None):
+    """p_target: [n_rows, vocab]; draft, parent, tokens, path: device int32 [n_rows]."""
+    vocab, dtype = p_target.shape[-1], p_target.dtype
+    i32 = torch.int32
+    _check(_lib.lora_verify_tree(verifier, _flat(p_target, n_rows * vocab, dtype, "p_target"), DTYPE_OF[dtype], vocab,
+                                 _flat(draft, n_rows, i32, "draft"), _flat(parent, n_rows, i32, "parent"),
+                                 _flat(row0, n_seqs + 1, i32, "row0"), _flat(u, n_rows, torch.float32, "u"), n_seqs,
+                                 n_rows, _flat(tokens, n_rows, i32, "tokens"), _flat(path, n_rows, i32, "path"),
+                                 _flat(accepted, n_seqs, i32, "accepted"), _stream(stream)), "lora_verify_tree")
 
 
 def lora_scorer_create(max_rows):

@@ -17,6 +17,8 @@ def test_tree_planner(tmp_path, flags):
 def test_null_handles():
     b = lora.lora_attend_batch()
     assert lora.raw_lib().lora_attend_plan_set_tree(None, None, ctypes.byref(b), None, None) == lora.LORA_EINVAL
+    assert lora.raw_lib().lora_verify_tree(None, None, 0, 8, None, None, None, None, 1, 1, None, None, None,
+                                           None) == lora.LORA_EINVAL
 
 
 def test_binding_refuses():

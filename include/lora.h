@@ -668,7 +668,8 @@ int lora_verify(lora_verifier v, const void *p_target, const void *p_draft, lora
  * accepted is -1, and the sequence's tokens and path are, where a row on the
  * way has no weight (no entry above 0, or a sum that is not finite); also, with
  * nothing else written, where the sequence's two entries of row0 do not ascend
- * or leave no row for each sequence before and after it.
+ * or leave no row for each sequence before and after it.  (Sequences that share
+ * rows, where a list does not ascend elsewhere, have no answer in particular.)
  * Errors (nothing enqueued): LORA_EINVAL, LORA_ETOKENS (n_seqs), LORA_EHIP.
  * Calls on one verifier on different streams are ordered by the caller. */
 int lora_verify_tree(lora_verifier v, const void *p_target, lora_dtype dtype, int vocab, const int32_t *draft,

@@ -23,7 +23,8 @@ ARCH = "gfx950"
 
 SOURCES = ["api.cpp", "ledger.cpp", "residency.cpp", "route.hip", "pad_copy.hip", "apply_kernels.hip", "gemm_decode.hip",
            "gemm_tiled.hip", "shrink_expand.hip", "scratch.hip", "kv_api.cpp", "attend_plan.cpp", "kv_cache.hip",
-           "attend.hip", "verify.hip", "logprobs.hip"]
+           "attend.hip", "verify.hip", "verify_tree.hip",
+           "logprobs.hip"]
 CALIB_SOURCES = ["calibrate.hip"]
 
 # Packed-fp32 VALU instructions are kept out of every device object.

@@ -26,6 +26,7 @@ static_assert(LORA_VERIFY_MAX_VOCAB == lora::VERIFY_PART * lora::VERIFY_PARTS, "
 static_assert(LORA_SCORE_MAX_TOP == lora::LOGPROBS_MAX_TOP, "the kernels have room for so many");
 static_assert(LORA_VERIFY_MAX_VOCAB == 256 * 128 * lora::LOGPROBS_MAX_PARTS, "a part is 32768 logits, or the whole row");
 static_assert(LORA_ROPE_MAX_AXES == lora::ROPE_MAX_AXES, "the kernels keep the positions of so many");
+static_assert(LORA_VERIFY_MAX_VOCAB == lora::VERIFY_CHUNKS * lora::VERIFY_MAX_SEGMENTS * 512, "a lane for each segment");
 static_assert(LORA_VERIFY_MAX_DRAFTS == lora::VERIFY_MAX_DRAFTS, "a lane for each drafted token");
 
 struct lora_kv_s {
@@ -77,6 +78,8 @@ struct lora_verifier_s {
     char *mem = nullptr;
     double *sums = nullptr;
     unsigned *count = nullptr;
+    double *row_sums = nullptr;
+    unsigned *row_count = nullptr;
 };
 
 namespace {
@@ -451,7 +454,9 @@ int lora_verifier_create(int max_seqs, lora_verifier *out) {
     if (v == nullptr) return LORA_ENOMEM;
     v->max_seqs = max_seqs;
     const size_t sums = static_cast<size_t>(max_seqs) * lora::VERIFY_PARTS * sizeof(double);
-    const size_t total = sums + static_cast<size_t>(max_seqs) * sizeof(unsigned);
+    const size_t count = align_up(static_cast<size_t>(max_seqs) * sizeof(unsigned), 256);
+    const size_t row_sums = static_cast<size_t>(lora::VERIFY_TREE_ROWS) * lora::VERIFY_CHUNKS * sizeof(double);
+    const size_t total = sums + count + row_sums + static_cast<size_t>(lora::VERIFY_TREE_ROWS) * sizeof(unsigned);
     hipError_t e = hipGetDevice(&v->device);
     if (e == hipSuccess) e = hipMalloc(reinterpret_cast<void **>(&v->mem), total);
     if (e == hipSuccess) e = hipMemset(v->mem, 0, total);
@@ -464,6 +469,8 @@ int lora_verifier_create(int max_seqs, lora_verifier *out) {
     }
     v->sums = reinterpret_cast<double *>(v->mem);
     v->count = reinterpret_cast<unsigned *>(v->mem + sums);
+    v->row_sums = reinterpret_cast<double *>(v->mem + sums + count);
+    v->row_count = reinterpret_cast<unsigned *>(v->mem + sums + count + row_sums);
     *out = v;
     return LORA_OK;
 }
@@ -542,7 +549,9 @@ int lora_verify_tree(lora_verifier v, const void *p_target, lora_dtype dtype, in
     a.n_seqs = n_seqs;
     a.n_rows = n_rows;
     a.vocab = vocab;
-    a.parts = (vocab + lora::VERIFY_PART - 1) / lora::VERIFY_PART;
+    a.sums = v->row_sums;
+    a.count_row = v->row_count;
+    a.count = v->count;
     HIP_TRY(lora::launch_verify_tree(a, static_cast<int>(dtype), static_cast<hipStream_t>(stream)));
     return LORA_OK;
 }

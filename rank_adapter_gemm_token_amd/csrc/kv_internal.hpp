@@ -110,8 +110,19 @@ struct VerifyTreeArgs {
     const int32_t *draft, *parent, *row0;
     const float *u;
     int32_t *tokens, *path, *accepted;
-    int n_seqs, n_rows, vocab, parts;
+    int n_seqs, n_rows, vocab;
+    // Where every row is drawn from at once, VERIFY_TREE_ROWS at most:
+    double *sums;          // [rows][VERIFY_CHUNKS]
+    unsigned *count_row;   // [rows], 0 between calls
+    unsigned *count;       // [seqs], 0 between calls
+    // Chosen by the launch: segments of a chunk, chunks of a workgroup (0: the
+    // sequences walk), whether it has few threads.
+    int segments, group;
+    bool few;
 };
+constexpr int VERIFY_TREE_ROWS = 4096;
+constexpr int VERIFY_CHUNKS = 64;        // of a row
+constexpr int VERIFY_MAX_SEGMENTS = 64;  // of a chunk
 
 hipError_t launch_verify_tree(const VerifyTreeArgs &a, int dtype, hipStream_t st);
 

@@ -132,6 +132,23 @@ def test_bounds_that_are_none(row0):
     lora.lora_verifier_destroy(v)
 
 
+def test_bounds_that_overlap():
+    """Sequences that share rows write over each other's answers, which are then
+    none in particular; ones whose own bounds are none have -1, ones that share
+    nothing their answer, and the next call is whole."""
+    p, draft, parent, row0, u = batch(["near"] * 4, [3, 3, 3, 3], 64, "f32", 1)
+    v = lora.lora_verifier_create(4)
+    for bad in ([0, 5, 3, 8, 12], [0, 8, 1, 10, 12], [0, 9, 2, 11, 4]):
+        accepted = call(p, draft, parent, bad, u, verifier=v)[2]
+        fits = [b <= bad[b] < bad[b + 1] <= 12 - (3 - b) for b in range(4)]
+        assert all(-1 <= a < 12 for a in accepted) and all(a == -1 for a, f in zip(accepted, fits) if not f)
+        if fits[3]:  # nobody else's rows reach into the last one's
+            assert accepted[3] == ref.verify_tree(p.double().cpu().numpy()[bad[3]:], draft[bad[3]:], parent[bad[3]:],
+                                                  [0, 12 - bad[3]], [np.float64(np.float32(x)) for x in u[bad[3]:]])[2][0]
+        assert call(p, draft, parent, row0, u, verifier=v) == same(p, draft, parent, row0, u)
+    lora.lora_verifier_destroy(v)
+
+
 @pytest.mark.parametrize("unit", [8, 512, 32768])
 def test_a_place_without_weight_is_not_drawn(unit):
     """As for lora_verify: weights whose order of adding decides about 1/2."""

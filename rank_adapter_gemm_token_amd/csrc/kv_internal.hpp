@@ -139,11 +139,11 @@ struct LogprobsArgs {
     uint64_t *keys;        // [rows][workgroups][LOGPROBS_MAX_TOP]
     float *stats;          // [rows][workgroups][4]
     unsigned *count;       // [rows], 0 between calls
-    // Chosen by the launch.
-    int threads, parts, group;
+    // Chosen by the launch: segments of a row, and of a workgroup.
+    int segments, group;
 };
 constexpr int LOGPROBS_MAX_TOP = 32;
-constexpr int LOGPROBS_MAX_PARTS = 64;  // parts of a row at most
+constexpr int LOGPROBS_MAX_PARTS = 64;  // workgroups of a row at most
 constexpr int LOGPROBS_WGS = 256;       // workgroups that rows are shared by at most
 
 hipError_t launch_logprobs(const LogprobsArgs &a, int dtype, hipStream_t st);

@@ -4,34 +4,30 @@
 // With c = scale * log2(e), the row's largest logit M and y_i = c (z_i - M):
 //     l = sum 2^y_i,   s = sum y_i 2^y_i,
 //     log p_i = ln 2 * (y_i - log2 l),   entropy = ln 2 * (log2 l - s / l).
-// A part of a row stands in the registers of one workgroup.  Every wave makes
-// l and s against its own largest logit, and they are joined once.
+// A row streams through a workgroup's waves once; every lane keeps its largest
+// logit, and l and s against it, and the lanes' are joined at the end.
 //
 // Alternatives are ordered by (logit descending, index ascending), one 64-bit
 // key an entry.  The k-th largest of the largest logits of 64 groups of lanes
-// is a bound that k entries reach, and few more do: these are listed, and each
-// entry's place is the number of those above it.  Where the list runs over (equal
-// logits, a vocabulary of a few hundred), the k-th largest of all lanes'
-// largest entries, with the index to tell equal ones apart, is a bound that
-// only k lanes reach.
+// is a bound that k entries reach, and few more do: the lanes that hold any look
+// for them once more, and each entry's place in their list is the number of
+// those above it.  Where the list runs over (equal logits, a vocabulary of a
+// few hundred), the k-th largest of what it holds is the next bound.
 #include "dtype.hpp"
 #include "kv_internal.hpp"
+#include "row_eight.hpp"
 
 namespace lora {
 
 namespace {
 
-constexpr int STEP = 8;          // neighbouring logits of a thread
-constexpr int ROUNDS = 4;        // of these
+constexpr int STEP = 8;          // neighbouring logits of a lane
+constexpr int SEGMENT = 64 * STEP;
+constexpr int AHEAD = 4;         // segments that a wave asks for together
 constexpr int GROUPS = 64;       // of lanes, whose largest logits give the first bound
-constexpr int LIST = 256;        // entries that the first bound may leave
-constexpr int ROOM = LOGPROBS_MAX_PARTS * LOGPROBS_MAX_TOP;  // and that there is room for
-static_assert(ROOM >= LOGPROBS_MAX_TOP * (STEP * ROUNDS + 1), "the entries of as many lanes, and those of the parts before");
-
-template <int DT>
-struct Wide {
-    typename Elem<DT>::raw w[STEP];
-};
+constexpr int LIST = 256;        // entries that a bound may leave
+constexpr int ROOM = 2 * LIST;   // entries listed of those that are too many
+static_assert(LIST > LOGPROBS_MAX_TOP, "the next bound is above the one before");
 
 // The bits of a float that 16-bit logits leave 0.
 template <int DT>
@@ -105,16 +101,25 @@ __device__ __forceinline__ Stats join(const Stats &a, const Stats &b, float c) {
     return Stats{m, a.l * ea + b.l * eb, a.s * ea + product(a.l * ea, ya) + b.s * eb + product(b.l * eb, yb)};
 }
 
-template <int THREADS>
+// The same of all lanes' (a lane without any: -inf, 0, 0).
+__device__ __forceinline__ Stats join_lanes(const Stats &a, float c) {
+    const float m = over64(a.m, Max()), ref = m == -INFINITY ? 0.0f : m;
+    const float y = (a.m - ref) * c, e = exp2_fast(y), l = a.l * e;
+    return Stats{m, over64(l, Sum()), over64(a.s * e + product(l, y), Sum())};
+}
+
+// What a workgroup's waves tell each other.
+template <int N>
 struct Shared {
-    uint64_t list[ROOM];                // entries; those of the parts before come first
-    uint64_t best[LOGPROBS_MAX_TOP];    // the largest so far, in order
+    uint64_t list[LOGPROBS_MAX_PARTS * LOGPROBS_MAX_TOP];  // entries, ROOM of them, or of all workgroups of the row
+    uint64_t best[LOGPROBS_MAX_TOP];                       // the largest, in order
     uint64_t bound;
-    uint32_t group[GROUPS];             // largest logits of the lanes' groups, as order_of
-    Stats wave[THREADS / 64];
-    int n;                              // entries in the list
+    uint32_t group[GROUPS];  // largest logits of the lanes' groups, as order_of
+    Stats wave[N / 64];
+    int n;                   // entries in the list
     unsigned arrived;
 };
+static_assert(ROOM <= LOGPROBS_MAX_PARTS * LOGPROBS_MAX_TOP, "one array serves both");
 
 // The k-th largest of 64 lanes' values, of which the lowest LOW bits are alike.
 template <int LOW>
@@ -129,9 +134,9 @@ __device__ __forceinline__ uint32_t kth_of_lanes(uint32_t v, int k) {
 }
 
 // Each entry's place among the n of the list: put(place, entry) for the first k.
-template <int THREADS, typename Put>
+template <int N, typename Put>
 __device__ __forceinline__ void rank(const uint64_t *list, int n, int k, Put put) {
-    for (int t = threadIdx.x; t < n; t += THREADS) {
+    for (int t = threadIdx.x; t < n; t += N) {
         const uint64_t mine = list[t];
         int place = 0;
         for (int j = 0; j < n; ++j) place += list[j] > mine;
@@ -139,245 +144,159 @@ __device__ __forceinline__ void rank(const uint64_t *list, int n, int k, Put put
     }
 }
 
-// The logits of one part of a row, in the workgroup's registers: thread t has
-// entries (round * THREADS + t) * 8 .. + 7 of the part.
-template <int DT, int THREADS>
-struct Part {
-    Wide<DT> z[ROUNDS];
-    int base, V;
+// Segments s0 .. s1 - 1 of a row of V logits, of which wave w has every N / 64th
+// from s0 + w on.
+template <int DT, int N>
+struct Row {
+    using raw = typename Elem<DT>::raw;
+    static constexpr int WAVES = N / 64;
+    static constexpr raw NONE = DT == DT_F32 ? 0xFF800000u : DT == DT_F16 ? 0xFC00u : 0xFF80u;  // -inf
+    const raw *z;
+    int V, s0, s1;
 
-    __device__ __forceinline__ int index(int k) const {
-        return base + (k * THREADS + static_cast<int>(threadIdx.x)) * STEP;
-    }
-    // Whether all lanes of the wave hold 8 logits of round k.
-    __device__ __forceinline__ bool whole(int k) const {
-        return uniform(base + (k * THREADS + static_cast<int>(threadIdx.x | 63)) * STEP + STEP) <= V;
-    }
-    __device__ __forceinline__ void load(const typename Elem<DT>::raw *row, int part, int vocab) {
-        base = part * THREADS * STEP * ROUNDS;
-        V = vocab;
+    using Batch = Eight<DT>[AHEAD];
+
+    // The lane's logits of AHEAD of the wave's segments from s on; -inf past the end.
+    __device__ __forceinline__ void load(Batch &e, int s) const {
+        const unsigned lane = threadIdx.x & 63;
+        const int last = s + (AHEAD - 1) * WAVES;
+        if (last < s1 && (last + 1) * SEGMENT <= V) {  // uniform
 #pragma unroll
-        for (int k = 0; k < ROUNDS; ++k) {
-            const int i = index(k);
-            // Rows start at any element, so the load is as wide as the
-            // hardware makes of an unaligned one.  Past the end: NaN, which no
-            // comparison takes.
-            if (i + STEP <= V) {
-                __builtin_memcpy(&z[k], row + i, sizeof z[k]);
-            } else {
+            for (int k = 0; k < AHEAD; ++k)
+                __builtin_memcpy(e[k].w, z + (s + k * WAVES) * SEGMENT + lane * STEP, sizeof e[k].w);
+            asm volatile("");  // a branch
+        } else {
+            auto index = [&](int k) {
+                return s + k * WAVES < s1 ? (s + k * WAVES) * SEGMENT + static_cast<int>(lane) * STEP : V;
+            };
 #pragma unroll
-                for (int j = 0; j < STEP; ++j) z[k].w[j] = i + j < V ? row[i + j] : Elem<DT>::qnan;
-            }
+            for (int k = 0; k < AHEAD; ++k) e[k].load(z, index(k), V);
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) e[k].clear(index(k), V, NONE);
         }
     }
-    // What was made of the logits is made anew: kept, it would take more
-    // registers than two workgroups a CU have.
-    __device__ __forceinline__ void forget() {
-#pragma unroll
-        for (int k = 0; k < ROUNDS; ++k) {
-            uint32_t w[sizeof z[k] / 4];
-            __builtin_memcpy(w, &z[k], sizeof w);
-#pragma unroll
-            for (uint32_t &x : w) asm volatile("" : "+v"(x));
-            __builtin_memcpy(&z[k], w, sizeof w);
-        }
-    }
-    __device__ __forceinline__ float at(int k, int j) const { return Elem<DT>::to_f(z[k].w[j]); }
-    // -inf where there is none.
-    __device__ __forceinline__ float at_or_none(int k, int j) const { return index(k) + j < V ? at(k, j) : -INFINITY; }
 
-    __device__ __forceinline__ float largest() const {
+    // The lane's l and s of a batch, against its largest logit m.
+    static __device__ __forceinline__ Stats stats(const Batch &e, float c) {
         float m = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < ROUNDS; ++k) {
-            if (whole(k)) {
+        for (int k = 0; k < AHEAD; ++k)
 #pragma unroll
-                for (int j = 0; j < STEP; ++j) m = fmaxf(m, at(k, j));
-            } else {
-#pragma unroll
-                for (int j = 0; j < STEP; ++j) m = fmaxf(m, at_or_none(k, j));
-            }
-        }
-        return m;
-    }
-
-    // The wave's l and s against its largest logit m.
-    __device__ __forceinline__ Stats stats(float m, float c) const {
-        float l = 0.0f, s = 0.0f;
+            for (int j = 0; j < STEP; ++j) m = fmaxf(m, e[k].at(j));
         const float mc = m * c;
-        if (fabsf(mc) < 1048576.0f) {
+        float l = 0.0f, s = 0.0f;
+        if (__all(fabsf(mc) < 1048576.0f)) {
             // y against mc, which is off m c by `off`: one rounding a logit.
-            const float off = fmaf(m, c, -mc);
+            const float off = fmaf(m, c, -mc), less = exp2_fast(-off);
 #pragma unroll
-            for (int k = 0; k < ROUNDS; ++k) {
-                if (whole(k)) {
+            for (int k = 0; k < AHEAD; ++k)
 #pragma unroll
-                    for (int j = 0; j < STEP; ++j) {
-                        const float y = fmaf(at(k, j), c, -mc), e = exp2_fast(y);
-                        l += e;
-                        s = fmaf(e, y, s);
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < STEP; ++j) {
-                        const float y = fmaf(at_or_none(k, j), c, -mc), e = exp2_fast(y);
-                        l += e;
-                        s += product(e, y);
-                    }
+                for (int j = 0; j < STEP; ++j) {
+                    const float y = fmaf(e[k].at(j), c, -mc), x = exp2_fast(y);
+                    l += x;
+                    s = fmaf(x, y, s);
                 }
-            }
-            s -= off * l;
-            const float less = exp2_fast(-off);
+            s = (s - off * l) * less;
             l *= less;
-            s *= less;
             // A logit of -inf makes s NaN, and not l.
-            if (!__any(s != s)) return Stats{m, over64(l, Sum()), over64(s, Sum())};
+            if (!__any(s != s)) return Stats{m, l, s};
             l = s = 0.0f;
         }
         const float ref = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-        for (int k = 0; k < ROUNDS; ++k)
+        for (int k = 0; k < AHEAD; ++k)
 #pragma unroll
             for (int j = 0; j < STEP; ++j) {
-                const float y = (at_or_none(k, j) - ref) * c, e = exp2_fast(y);
-                l += e;
-                s += product(e, y);
+                const float y = (e[k].at(j) - ref) * c, x = exp2_fast(y);
+                l += x;
+                s += product(x, y);
             }
-        return Stats{m, over64(l, Sum()), over64(s, Sum())};
+        return Stats{m, l, s};
     }
 
-    // Adds the thread's entries of at least `bound` (none of them is below the
-    // logit `low`) to the list, as far as there is room.
-    __device__ __forceinline__ void list_those(uint64_t *list, int *n, float low, uint64_t bound) const {
-#pragma unroll
-        for (int k = 0; k < ROUNDS; ++k)
-#pragma unroll
-            for (int j = 0; j < STEP; ++j) {
-                const float v = at(k, j);
-                if (v >= low) {
-                    const uint64_t key = key_of(v, index(k) + j);
-                    const int to = key >= bound ? atomicAdd(n, 1) : ROOM;
-                    if (to < ROOM) list[to] = key;
+    // The lane's l and s of all its logits.
+    __device__ __forceinline__ Stats read(float c) const {
+        Stats all{-INFINITY, 0.0f, 0.0f};
+        for (int s = s0 + uniform(threadIdx.x >> 6); s < s1; s += AHEAD * WAVES) {
+            Batch e;
+            load(e, s);
+            all = join(all, stats(e, c), c);
+        }
+        return all;
+    }
+
+    // Adds the entries of at least `bound` that the wave's lanes in `lanes` hold
+    // to the list, as long as there are not too many.  The wave looks through one
+    // such lane's logits after the other, an entry a lane (every lane through its
+    // own: 2048 rows of 32000 took 44 us).
+    __device__ __forceinline__ void list(unsigned long long lanes, uint64_t bound, uint64_t *to, int *n) const {
+        const int lane = threadIdx.x & 63, from = s0 + uniform(threadIdx.x >> 6);
+        const int entries = from < s1 ? ((s1 - 1 - from) / WAVES + 1) * STEP : 0;
+        for (; lanes != 0; lanes &= lanes - 1) {
+            const int whose = __builtin_ctzll(lanes);
+            for (int e = lane; e < entries; e += 64) {
+                const int i = (from + e / STEP * WAVES) * SEGMENT + whose * STEP + e % STEP;
+                const float v = i < V ? Elem<DT>::to_f(z[i]) : __uint_as_float(Elem<DT_F32>::qnan);
+                if (v == v && key_of(v, i) >= bound) {
+                    const int place = atomicAdd(n, 1);
+                    if (place < ROOM) to[place] = key_of(v, i);
                 }
             }
-    }
-
-    // The first of the thread's logits that are its largest, m.
-    __device__ __forceinline__ int first_of(float m) const {
-        int i = V;
-#pragma unroll
-        for (int k = ROUNDS - 1; k >= 0; --k)
-#pragma unroll
-            for (int j = STEP - 1; j >= 0; --j) i = at(k, j) == m ? index(k) + j : i;
-        return i;
+            if (__hip_atomic_load(n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) > ROOM) break;
+        }
     }
 };
 
-// Workgroup (row, c) takes parts c * group .. of the row, one after the other;
-// the last of a row's workgroups to finish joins what they found.
-template <int DT, int THREADS>
-__global__ __launch_bounds__(THREADS, 8) void k_logprobs(LogprobsArgs a) {
-    using raw = typename Elem<DT>::raw;
-    constexpr int WAVES = THREADS / 64, LOW = low_bits<DT>();
-    __shared__ Shared<THREADS> sh;
-    const int row = blockIdx.x, t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
-    const raw *z = static_cast<const raw *>(a.z) + row * a.stride;
-    const int top = a.top;
-    const int token = a.tokens != nullptr ? a.tokens[row] : -1;
-    const bool known = token >= 0 && token < a.vocab;
-    const float zt = known ? Elem<DT>::to_f(z[token]) : 0.0f;
-
-    Stats all{-INFINITY, 0.0f, 0.0f};
-    int n_best = 0;  // entries of sh.best
-    const int p0 = blockIdx.y * a.group, p1 = p0 + a.group < a.parts ? p0 + a.group : a.parts;
-    Part<DT, THREADS> part;
-    for (int p = p0; p < p1; ++p) {
-        part.load(z, p, a.vocab);
-        if (t < n_best) sh.list[t] = sh.best[t];
-        if (t == 0) sh.n = n_best;
-        const float mine = part.largest();
-        const float of_group = THREADS == 1024 ? over16(mine, Max()) : over4(mine, Max());
-        if (t % (THREADS / GROUPS) == 0) sh.group[t / (THREADS / GROUPS)] = order_of(of_group);
-        part.forget();
-        const Stats st = part.stats(over64(of_group, Max()), a.c);
-        part.forget();
-        if (lane == 0) sh.wave[wave] = st;
+// What workgroup blockIdx.y of a row found, to the agent's coherence point; the
+// workgroup that is counted last joins all of them, in sh.best and (first wave)
+// in `all`.
+template <int N>
+__device__ __forceinline__ bool last_of_row(const LogprobsArgs &a, Shared<N> &sh, int row, int n_best, Stats &all) {
+    const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6), wgs = gridDim.y, top = a.top;
+    uint64_t *keys = a.keys + static_cast<long>(row) * wgs * LOGPROBS_MAX_TOP;
+    float *stats = a.stats + static_cast<long>(row) * wgs * 4;
+    if (wave == 0) {
+        if (lane < top)
+            __hip_atomic_store(keys + blockIdx.y * LOGPROBS_MAX_TOP + lane, lane < n_best ? sh.best[lane] : 0,
+                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (lane < 3)
+            __hip_atomic_store(stats + blockIdx.y * 4 + lane, lane == 0 ? all.m : lane == 1 ? all.l : all.s,
+                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        if (lane == 0)
+            sh.arrived = __hip_atomic_fetch_add(a.count + row, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    if (sh.arrived != static_cast<unsigned>(wgs) - 1) return false;
+    if (t == 0) {
+        __hip_atomic_store(a.count + row, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        sh.n = 0;
+    }
+    if (wave == 0) {
+        const float *from = stats + (lane < wgs ? lane : 0) * 4;
+        auto get = [&](int i) { return __hip_atomic_load(from + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
+        const Stats there{get(0), get(1), get(2)};
+        all = join_lanes(lane < wgs ? there : Stats{-INFINITY, 0.0f, 0.0f}, a.c);
+    }
+    if (top > 0) {
         __syncthreads();
-#pragma unroll 1
-        for (int w = 0; w < WAVES; ++w) all = join(all, sh.wave[w], a.c);
-        if (top > 0) {
-            // At least `top` entries of the part reach the bound, if it has as many.
-            const float low = of_order(kth_of_lanes<LOW>(sh.group[lane], top));
-            if (mine >= low) part.list_those(sh.list, &sh.n, low, 0);
-            __syncthreads();
-            if (sh.n > LIST) {
-                __syncthreads();
-                if (t == 0) sh.n = n_best, sh.bound = 0;
-                __syncthreads();
-                part.forget();
-                const int first = mine >= low ? part.first_of(mine) : a.vocab;
-                const uint64_t entry = first < a.vocab ? key_of(mine, first) : 0;
-                if (entry != 0) sh.list[atomicAdd(&sh.n, 1)] = entry;
-                __syncthreads();
-                rank<THREADS>(sh.list, sh.n, top, [&](int place, uint64_t key) {
-                    if (place == top - 1) sh.bound = key;
-                });
-                __syncthreads();
-                const uint64_t bound = sh.bound;
-                if (t == 0) sh.n = n_best;
-                __syncthreads();
-                part.forget();
-                if (entry >= bound && entry != 0) part.list_those(sh.list, &sh.n, low, bound);
-                __syncthreads();
-            }
-            const int n = sh.n;
-            rank<THREADS>(sh.list, n, top, [&](int place, uint64_t key) { sh.best[place] = key; });
-            n_best = n < top ? n : top;
+        for (int i = t; i < wgs * top; i += N) {
+            const uint64_t key = __hip_atomic_load(keys + i / top * LOGPROBS_MAX_TOP + i % top, __ATOMIC_RELAXED,
+                                                   __HIP_MEMORY_SCOPE_AGENT);
+            if (key != 0) sh.list[atomicAdd(&sh.n, 1)] = key;
         }
+        __syncthreads();
+        rank<N>(sh.list, sh.n, top, [&](int place, uint64_t key) { sh.best[place] = key; });
         __syncthreads();
     }
+    return true;
+}
 
-    if (gridDim.y > 1) {
-        // What this workgroup found, to the agent's coherence point; then it is counted.
-        const int wgs = gridDim.y;
-        uint64_t *keys = a.keys + (static_cast<long>(row) * wgs + blockIdx.y) * LOGPROBS_MAX_TOP;
-        float *stats = a.stats + (static_cast<long>(row) * wgs + blockIdx.y) * 4;
-        if (wave == 0) {
-            if (lane < top)
-                __hip_atomic_store(keys + lane, lane < n_best ? sh.best[lane] : 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            if (lane < 3)
-                __hip_atomic_store(stats + lane, lane == 0 ? all.m : lane == 1 ? all.l : all.s, __ATOMIC_RELAXED,
-                                   __HIP_MEMORY_SCOPE_AGENT);
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            if (lane == 0)
-                sh.arrived = __hip_atomic_fetch_add(a.count + row, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        }
-        __syncthreads();
-        if (sh.arrived != static_cast<unsigned>(wgs) - 1) return;
-        if (t == 0) {
-            __hip_atomic_store(a.count + row, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            sh.n = 0;
-        }
-        all = Stats{-INFINITY, 0.0f, 0.0f};
-        const float *from = a.stats + static_cast<long>(row) * wgs * 4;
-        for (int w = 0; w < wgs; ++w) {
-            auto get = [&](int i) { return __hip_atomic_load(from + w * 4 + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
-            all = join(all, Stats{get(0), get(1), get(2)}, a.c);
-        }
-        if (top > 0) {
-            __syncthreads();
-            for (int i = t; i < wgs * top; i += THREADS) {
-                const uint64_t key = __hip_atomic_load(
-                    a.keys + (static_cast<long>(row) * wgs + i / top) * LOGPROBS_MAX_TOP + i % top, __ATOMIC_RELAXED,
-                    __HIP_MEMORY_SCOPE_AGENT);
-                if (key != 0) sh.list[atomicAdd(&sh.n, 1)] = key;
-            }
-            __syncthreads();
-            rank<THREADS>(sh.list, sh.n, top, [&](int place, uint64_t key) { sh.best[place] = key; });
-            __syncthreads();
-        }
-    }
-
+// A row's results, by one wave.
+template <int DT>
+__device__ __forceinline__ void put(const LogprobsArgs &a, int row, const Stats &all, const uint64_t *best, bool known,
+                                    float zt) {
+    const int lane = threadIdx.x & 63;
     // No distribution: something is no number, or nothing is above -inf.
     const bool none = !(all.l > 0.0f && all.l < INFINITY) || !(fabsf(all.m) < INFINITY);
     constexpr double LN2 = 0.69314718055994530942;
@@ -386,27 +305,79 @@ __global__ __launch_bounds__(THREADS, 8) void k_logprobs(LogprobsArgs a) {
     int exponent;
     const float left = frexpf(all.l, &exponent);
     const double log_l = static_cast<double>(exponent) + static_cast<double>(__log2f(left));
-    auto log_p = [&](float v) {
-        const double y = (static_cast<double>(v) - static_cast<double>(all.m)) * static_cast<double>(a.c);
-        return none ? nan : static_cast<float>(LN2 * (y - log_l));
-    };
-    if (t == 0) {
-        if (a.logprob != nullptr) a.logprob[row] = known ? log_p(zt) : nan;
+    // Lane `top` has the given token.
+    const uint64_t key = lane < a.top ? best[lane] : 0;
+    const float v = lane < a.top ? of_order(static_cast<uint32_t>(key >> 32)) : zt;
+    const double y = (static_cast<double>(v) - static_cast<double>(all.m)) * static_cast<double>(a.c);
+    const float log_p = none ? nan : static_cast<float>(LN2 * (y - log_l));
+    if (lane < a.top) {
+        const long at = static_cast<long>(row) * a.top + lane;
+        a.top_ids[at] = none ? -1 : static_cast<int32_t>(~static_cast<uint32_t>(key));
+        a.top_logprobs[at] = log_p;
+    } else if (lane == a.top) {
+        if (a.logprob != nullptr) a.logprob[row] = known ? log_p : nan;
         if (a.entropy != nullptr)
             a.entropy[row] = none ? nan : static_cast<float>(LN2 * (log_l - static_cast<double>(all.s) / static_cast<double>(all.l)));
     }
-    if (t < top) {
-        const uint64_t key = sh.best[t];
-        const long at = static_cast<long>(row) * top + t;
-        a.top_ids[at] = none ? -1 : static_cast<int32_t>(~static_cast<uint32_t>(key));
-        a.top_logprobs[at] = log_p(of_order(static_cast<uint32_t>(key >> 32)));
+}
+
+// Workgroup (row, c) reads `group` segments of a row from c * group on; the last
+// of a row's workgroups to finish joins what they found.
+template <int DT, int N>
+__global__ __launch_bounds__(N, 8) void k_logprobs(LogprobsArgs a) {
+    constexpr int WAVES = N / 64, LANES = N / GROUPS, LOW = low_bits<DT>();
+    static_assert(LANES == 4 || LANES == 16, "what the lanes are joined over");
+    __shared__ Shared<N> sh;
+    const int row = blockIdx.x, t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6), top = a.top;
+    Row<DT, N> r;
+    r.z = static_cast<const typename Elem<DT>::raw *>(a.z) + row * a.stride;
+    r.V = a.vocab;
+    r.s0 = blockIdx.y * a.group;
+    r.s1 = r.s0 + a.group < a.segments ? r.s0 + a.group : a.segments;
+    const int token = a.tokens != nullptr ? a.tokens[row] : -1;
+    const bool known = token >= 0 && token < a.vocab;
+    const float zt = known ? Elem<DT>::to_f(r.z[token]) : 0.0f;
+    if (t == 0) sh.n = 0;
+
+    const Stats mine = r.read(a.c);
+    const float of_group = LANES == 16 ? over16(mine.m, Max()) : over4(mine.m, Max());
+    if (t % LANES == 0) sh.group[t / LANES] = order_of(of_group);
+    const Stats of_wave = join_lanes(mine, a.c);
+    if (lane == 0) sh.wave[wave] = of_wave;
+    __syncthreads();
+    int n_best = 0;
+    if (top > 0) {
+        // At least `top` entries reach the bound, if there are as many.
+        uint64_t bound = static_cast<uint64_t>(kth_of_lanes<LOW>(sh.group[lane], top)) << 32;
+        for (;;) {
+            r.list(__ballot(order_of(mine.m) >= static_cast<uint32_t>(bound >> 32)), bound, sh.list, &sh.n);
+            __syncthreads();
+            const int n = sh.n;
+            if (n <= LIST) break;
+            // Too many: as many entries reach the `top`-th of those listed.
+            rank<N>(sh.list, n < ROOM ? n : ROOM, top, [&](int place, uint64_t key) {
+                if (place == top - 1) sh.bound = key;
+            });
+            __syncthreads();
+            bound = sh.bound;
+            if (t == 0) sh.n = 0;
+            __syncthreads();
+        }
+        const int n = sh.n;
+        rank<N>(sh.list, n, top, [&](int place, uint64_t key) { sh.best[place] = key; });
+        n_best = n < top ? n : top;
+        __syncthreads();
     }
+    Stats all{-INFINITY, 0.0f, 0.0f};
+    if (wave == 0) all = join_lanes(lane < WAVES ? sh.wave[lane] : all, a.c);
+    if (gridDim.y > 1 && !last_of_row<N>(a, sh, row, n_best, all)) return;
+    if (wave == 0) put<DT>(a, row, all, sh.best, known, zt);
 }
 
 template <int DT>
-hipError_t run(const LogprobsArgs &a, hipStream_t st) {
-    const dim3 grid(a.n_rows, (a.parts + a.group - 1) / a.group);
-    if (a.threads == 256)
+hipError_t run(const LogprobsArgs &a, bool few, hipStream_t st) {
+    const dim3 grid(a.n_rows, (a.segments + a.group - 1) / a.group);
+    if (few)
         k_logprobs<DT, 256><<<grid, 256, 0, st>>>(a);
     else
         k_logprobs<DT, 1024><<<grid, 1024, 0, st>>>(a);
@@ -417,17 +388,17 @@ hipError_t run(const LogprobsArgs &a, hipStream_t st) {
 
 hipError_t launch_logprobs(const LogprobsArgs &args, int dtype, hipStream_t st) {
     LogprobsArgs a = args;
-    // A vocabulary that four waves hold needs no more of them.
-    a.threads = a.vocab <= 256 * STEP * ROUNDS ? 256 : 1024;
-    const int held = a.threads * STEP * ROUNDS;
-    a.parts = (a.vocab + held - 1) / held;
-    // As many workgroups to a row as there are CUs for it.
-    const int wgs = LOGPROBS_WGS / a.n_rows;
-    a.group = wgs < 1 ? a.parts : (a.parts + wgs - 1) / wgs;
+    a.segments = (a.vocab + SEGMENT - 1) / SEGMENT;
+    const bool few = a.vocab <= 8192 || (a.n_rows >= 512 && a.vocab <= 1 << 18);
+    // As many workgroups to a row as there are CUs for it, of 64 segments each at least.
+    int wgs = LOGPROBS_WGS / a.n_rows, parts = (a.segments + 63) / 64;
+    if (few || wgs < 1) wgs = 1;
+    if (wgs > parts) wgs = parts;
+    a.group = (a.segments + wgs - 1) / wgs;
     switch (dtype) {
-        case DT_F32: return run<DT_F32>(a, st);
-        case DT_F16: return run<DT_F16>(a, st);
-        default: return run<DT_BF16>(a, st);
+        case DT_F32: return run<DT_F32>(a, few, st);
+        case DT_F16: return run<DT_F16>(a, few, st);
+        default: return run<DT_BF16>(a, few, st);
     }
 }
 

@@ -11,6 +11,7 @@
 // lanes.  Only the chunk that is drawn from is read again (a few KB).
 #include "dtype.hpp"
 #include "kv_internal.hpp"
+#include "row_eight.hpp"
 #include "wave_fp64.hpp"
 
 namespace lora {
@@ -23,23 +24,17 @@ constexpr int CHUNKS = VERIFY_CHUNKS;
 constexpr int AHEAD = 4;          // segments a wave asks for together (8: a walk over 131072 entries 92 us instead of 89)
 static_assert(CHUNKS == 64, "a lane for each");
 
+// Entries i .. i + 7 of a row of V as weights: what is not above zero (NaN, what
+// is past the end) counts as nothing.
 template <int DT>
-struct Wide {
-    typename Elem<DT>::raw w[STEP];
-
-    // Entries i .. i + 7 of a row of V; 0 where there is none.
-    __device__ __forceinline__ void load(const typename Elem<DT>::raw *row, int i, int V) {
-        // Rows start at any entry, so the load is as wide as the hardware
-        // makes of an unaligned one.
-        if (i + STEP <= V) {
-            __builtin_memcpy(this, row + i, sizeof *this);
-        } else {
-#pragma unroll
-            for (int j = 0; j < STEP; ++j) w[j] = i + j < V ? row[i + j] : 0;
-        }
+struct Weights {
+    Eight<DT> e;
+    __device__ __forceinline__ void load(const typename Elem<DT>::raw *row, int i, int V) { e.load(row, i, V); }
+    // After load(); `whole`: no lane of the wave looks past the end.
+    __device__ __forceinline__ void clear(int i, int V, bool whole) {
+        if (!whole) e.clear(i, V, 0);
     }
-    // A weight: what is not above zero (NaN among it) counts as nothing.
-    __device__ __forceinline__ double at(int j) const { return static_cast<double>(fmaxf(Elem<DT>::to_f(w[j]), 0.0f)); }
+    __device__ __forceinline__ double at(int j) const { return static_cast<double>(fmaxf(e.at(j), 0.0f)); }
     __device__ __forceinline__ double sum() const {
         double v = 0.0;
 #pragma unroll
@@ -74,16 +69,18 @@ struct Row {
         int c = c0 + wave, s = 0;  // the next segment
         double acc = 0.0;
         while (c < c1) {
-            Wide<DT> w[AHEAD];
-            int cc = c, ss = s;
+            Weights<DT> w[AHEAD];
+            int cc = c, ss = s, at[AHEAD];
 #pragma unroll
             for (int k = 0; k < AHEAD; ++k) {
-                w[k].load(p, cc < c1 ? (cc * segments + ss) * SEGMENT + lane * STEP : V, V);
+                at[k] = cc < c1 ? (cc * segments + ss) * SEGMENT : V;
+                w[k].load(p, at[k] + lane * STEP, V);
                 if (++ss == segments) ss = 0, cc += WAVES;
             }
 #pragma unroll
             for (int k = 0; k < AHEAD; ++k) {
                 if (c >= c1) break;
+                w[k].clear(at[k] + lane * STEP, V, at[k] + SEGMENT <= V);
                 acc += w[k].sum();
                 if (++s == segments) {
                     const double all = wave_sum(acc);
@@ -109,8 +106,10 @@ struct Row {
         int s = 0;
         if (segments > 1) {
             for (int i = wave; i < segments; i += WAVES) {
-                Wide<DT> w;
-                w.load(p, (c * segments + i) * SEGMENT + lane * STEP, V);
+                const int at = (c * segments + i) * SEGMENT;
+                Weights<DT> w;
+                w.load(p, at + lane * STEP, V);
+                w.clear(at + lane * STEP, V, at + SEGMENT <= V);
                 const double all = wave_sum(w.sum());
                 if (lane == 0) sh.segment[i] = all;
             }
@@ -121,9 +120,10 @@ struct Row {
             if (s > 0) base = lane_of(run, s - 1);
         }
         if (wave == 0) {
-            const int i = (c * segments + s) * SEGMENT + lane * STEP;
-            Wide<DT> w;
+            const int i = (c * segments + s) * SEGMENT + lane * STEP, first = V < STEP ? 0 : Eight<DT>::first(i, V);
+            Weights<DT> w;
             w.load(p, i, V);
+            w.clear(i, V, false);
             const double mine = w.sum(), upto = base + wave_scan(mine);
             const int l = pick_lane(mine, upto, aim);
             if (l > 0) base = lane_of(upto, l - 1);
@@ -133,8 +133,8 @@ struct Row {
                 for (int j = 0; j < STEP; ++j) {
                     const double x = w.at(j);
                     base += x;
-                    if (x > 0.0) last = i + j;
-                    if (hit < 0 && x > 0.0 && base > aim) hit = i + j;
+                    if (x > 0.0) last = first + j;
+                    if (hit < 0 && x > 0.0 && base > aim) hit = first + j;
                 }
                 sh.token = hit >= 0 ? hit : last;  // last: rounding kept the sum at or below the aim
             }
@@ -334,10 +334,11 @@ hipError_t launch_verify_tree(const VerifyTreeArgs &args, int dtype, hipStream_t
     if (a.n_rows <= VERIFY_TREE_ROWS && rows <= walk) {
         // Many rows: small workgroups, eight a CU, whose loads and ends overlap
         // (1600 rows of 8000: 18 us instead of 28; 256 of 32000: 16.5 instead
-        // of 14.6); of long rows two a row (960 of 100000: 45 instead of 53).
+        // of 14.6); of long rows two a row (960 of 100000: 45 instead of 53,
+        // 610 of 131072: 41 instead of 58).
         // Few and long ones: up to four large workgroups a row (32 of 131072:
         // 10 us instead of 15; 256: 33 instead of 31).
-        a.few = a.n_rows >= 768 || a.vocab <= 4096;
+        a.few = a.n_rows >= 512 || a.vocab <= 4096;
         const int wgs = a.vocab <= 65536 ? 1 : a.few ? 2 : a.n_rows > 128 ? 1 : a.n_rows > 64 ? 2 : 4;
         a.group = CHUNKS / wgs;
     }

@@ -37,8 +37,9 @@ def check(z, tokens, scale, top, got, rows=None):
     """c (z - M) is rounded three times (c itself, the difference, and the part
     of M c that fp32 does not hold): 3 * 2^-24 of its own size, or of the 1 that
     the last may be.  A term 2^y is off by ln 2 of that and by the exponential's
-    2^-22; a sum of terms of one sign by 2^-24 for each of the 32 + 6 + 16 + 64
-    additions on a term's way.  In l that is relative, in the logarithm
+    2^-22; a sum of terms of one sign by 2^-24 for each of the additions on a
+    term's way, 120 at most (32 of a batch, those of batches, lanes, waves and
+    workgroups).  In l that is relative, in the logarithm
     absolute.  s is a sum of such terms times y, whose sizes add up to at most
     |log p| times p: the entropy's own terms; what e^y has lost is multiplied by
     y once more.  The result is rounded once."""

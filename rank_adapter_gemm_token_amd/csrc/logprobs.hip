@@ -111,11 +111,13 @@ __device__ __forceinline__ Stats join_lanes(const Stats &a, float c) {
 // What a workgroup's waves tell each other.
 template <int N>
 struct Shared {
-    uint64_t list[LOGPROBS_MAX_PARTS * LOGPROBS_MAX_TOP];  // entries, ROOM of them, or of all workgroups of the row
+    // Entries, ROOM of them, or of all workgroups of the row; 0 where there is none.
+    uint64_t list[LOGPROBS_MAX_PARTS * LOGPROBS_MAX_TOP];
     uint64_t best[LOGPROBS_MAX_TOP];                       // the largest, in order
     uint64_t bound;
     uint32_t group[GROUPS];  // largest logits of the lanes' groups, as order_of
     Stats wave[N / 64];
+    uint8_t lane[N / 64][64];  // of each wave: the lanes that hold entries to list
     int n;                   // entries in the list
     unsigned arrived;
 };
@@ -133,14 +135,21 @@ __device__ __forceinline__ uint32_t kth_of_lanes(uint32_t v, int k) {
     return bound & 0x80000000u ? bound : bound | ((1u << LOW) - 1u);
 }
 
-// Each entry's place among the n of the list: put(place, entry) for the first k.
+// Each entry's place among the n of the list (zeros among them, and up to a
+// multiple of 8, do no harm): put(place, entry) for the first k.
 template <int N, typename Put>
 __device__ __forceinline__ void rank(const uint64_t *list, int n, int k, Put put) {
     for (int t = threadIdx.x; t < n; t += N) {
         const uint64_t mine = list[t];
         int place = 0;
-        for (int j = 0; j < n; ++j) place += list[j] > mine;
-        if (place < k) put(place, mine);
+        for (int j = 0; j < n; j += 8) {  // read together: one by one, 80 entries took 3 us
+            uint64_t other[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) other[i] = list[j + i];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) place += other[i] > mine;
+        }
+        if (mine != 0 && place < k) put(place, mine);
     }
 }
 
@@ -225,23 +234,32 @@ struct Row {
         return all;
     }
 
-    // Adds the entries of at least `bound` that the wave's lanes in `lanes` hold
-    // to the list, as long as there are not too many.  The wave looks through one
-    // such lane's logits after the other, an entry a lane (every lane through its
-    // own: 2048 rows of 32000 took 44 us).
-    __device__ __forceinline__ void list(unsigned long long lanes, uint64_t bound, uint64_t *to, int *n) const {
+    // Adds the entries of at least `bound` that the wave's lanes with `mine` hold
+    // to the list, as long as there are not too many.  The wave looks through
+    // these lanes' logits together, LOOK of them a lane at a time (every lane
+    // through its own: 2048 rows of 32000 took 44 us).
+    __device__ __forceinline__ void list(bool mine, uint64_t bound, uint8_t *whose, uint64_t *to, int *n) const {
+        constexpr int LOOK = 4;
         const int lane = threadIdx.x & 63, from = s0 + uniform(threadIdx.x >> 6);
-        const int entries = from < s1 ? ((s1 - 1 - from) / WAVES + 1) * STEP : 0;
-        for (; lanes != 0; lanes &= lanes - 1) {
-            const int whose = __builtin_ctzll(lanes);
-            for (int e = lane; e < entries; e += 64) {
-                const int i = (from + e / STEP * WAVES) * SEGMENT + whose * STEP + e % STEP;
-                const float v = i < V ? Elem<DT>::to_f(z[i]) : __uint_as_float(Elem<DT_F32>::qnan);
-                if (v == v && key_of(v, i) >= bound) {
-                    const int place = atomicAdd(n, 1);
-                    if (place < ROOM) to[place] = key_of(v, i);
-                }
+        const unsigned long long some = __ballot(mine);
+        if (some == 0 || from >= s1) return;
+        if (mine) whose[__popcll(some & ((1ull << lane) - 1))] = static_cast<uint8_t>(lane);
+        const int segments = (s1 - 1 - from) / WAVES + 1, all = __popcll(some) * segments * STEP;
+        for (int q = lane; q - lane < all; q += LOOK * 64) {
+            int i[LOOK];
+            float v[LOOK];
+#pragma unroll
+            for (int k = 0; k < LOOK; ++k) {
+                const int at = q + k * 64, c = at / STEP / segments, s = at / STEP - c * segments;
+                i[k] = at < all ? (from + s * WAVES) * SEGMENT + whose[c & 63] * STEP + at % STEP : V;
+                v[k] = Elem<DT>::to_f(z[i[k] < V ? i[k] : V - 1]);
             }
+#pragma unroll
+            for (int k = 0; k < LOOK; ++k)
+                if (i[k] < V && v[k] == v[k] && key_of(v[k], i[k]) >= bound) {
+                    const int place = atomicAdd(n, 1);
+                    if (place < ROOM) to[place] = key_of(v[k], i[k]);
+                }
             if (__hip_atomic_load(n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) > ROOM) break;
         }
     }
@@ -268,10 +286,7 @@ __device__ __forceinline__ bool last_of_row(const LogprobsArgs &a, Shared<N> &sh
     }
     __syncthreads();
     if (sh.arrived != static_cast<unsigned>(wgs) - 1) return false;
-    if (t == 0) {
-        __hip_atomic_store(a.count + row, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        sh.n = 0;
-    }
+    if (t == 0) __hip_atomic_store(a.count + row, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if (wave == 0) {
         const float *from = stats + (lane < wgs ? lane : 0) * 4;
         auto get = [&](int i) { return __hip_atomic_load(from + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
@@ -279,14 +294,12 @@ __device__ __forceinline__ bool last_of_row(const LogprobsArgs &a, Shared<N> &sh
         all = join_lanes(lane < wgs ? there : Stats{-INFINITY, 0.0f, 0.0f}, a.c);
     }
     if (top > 0) {
+        for (int i = t; i < ((wgs * top + 7) & ~7); i += N)
+            sh.list[i] = i < wgs * top ? __hip_atomic_load(keys + i / top * LOGPROBS_MAX_TOP + i % top, __ATOMIC_RELAXED,
+                                                           __HIP_MEMORY_SCOPE_AGENT)
+                                       : 0;
         __syncthreads();
-        for (int i = t; i < wgs * top; i += N) {
-            const uint64_t key = __hip_atomic_load(keys + i / top * LOGPROBS_MAX_TOP + i % top, __ATOMIC_RELAXED,
-                                                   __HIP_MEMORY_SCOPE_AGENT);
-            if (key != 0) sh.list[atomicAdd(&sh.n, 1)] = key;
-        }
-        __syncthreads();
-        rank<N>(sh.list, sh.n, top, [&](int place, uint64_t key) { sh.best[place] = key; });
+        rank<N>(sh.list, wgs * top, top, [&](int place, uint64_t key) { sh.best[place] = key; });
         __syncthreads();
     }
     return true;
@@ -338,6 +351,7 @@ __global__ __launch_bounds__(N, 8) void k_logprobs(LogprobsArgs a) {
     const bool known = token >= 0 && token < a.vocab;
     const float zt = known ? Elem<DT>::to_f(r.z[token]) : 0.0f;
     if (t == 0) sh.n = 0;
+    for (int i = t; i < ROOM; i += N) sh.list[i] = 0;
 
     const Stats mine = r.read(a.c);
     const float of_group = LANES == 16 ? over16(mine.m, Max()) : over4(mine.m, Max());
@@ -350,7 +364,7 @@ __global__ __launch_bounds__(N, 8) void k_logprobs(LogprobsArgs a) {
         // At least `top` entries reach the bound, if there are as many.
         uint64_t bound = static_cast<uint64_t>(kth_of_lanes<LOW>(sh.group[lane], top)) << 32;
         for (;;) {
-            r.list(__ballot(order_of(mine.m) >= static_cast<uint32_t>(bound >> 32)), bound, sh.list, &sh.n);
+            r.list(order_of(mine.m) >= static_cast<uint32_t>(bound >> 32), bound, sh.lane[wave], sh.list, &sh.n);
             __syncthreads();
             const int n = sh.n;
             if (n <= LIST) break;
@@ -361,6 +375,7 @@ __global__ __launch_bounds__(N, 8) void k_logprobs(LogprobsArgs a) {
             __syncthreads();
             bound = sh.bound;
             if (t == 0) sh.n = 0;
+            for (int i = t; i < ROOM; i += N) sh.list[i] = 0;
             __syncthreads();
         }
         const int n = sh.n;

@@ -191,7 +191,7 @@ __device__ __forceinline__ void join_parts(const AttendArgs &a, const AttendToke
         const int p = j < tk.n[0] ? tk.part[0] + j * tk.stride[0] : tk.part[1] + (j - tk.n[0]) * tk.stride[1];
         return static_cast<long>(p) * a.heads + head;
     };
-    constexpr int STEP = 4;  // results asked for together
+    constexpr int STEP = ATTEND_JOIN_STEP;  // results asked for together
     float M = -INFINITY, L = 0.0f;
     f32x4_t sum{0.0f, 0.0f, 0.0f, 0.0f};
     for (int j = 0; j < n; j += STEP) {
@@ -707,23 +707,28 @@ hipError_t run(const AttendArgs &a, int n_groups, int n_tokens, hipStream_t st) 
 // and its count before it ends, which is paid where workgroups share a CU or
 // follow one another on it (64 sequences with drafts, 448 workgroups: 59 us
 // instead of 55; 64 decoding ones, 1200: 49 instead of 43).  So: up to one a
-// CU.
-constexpr int JOIN_HERE_WGS = 256;
+// CU.  And the last of a block joins one token after the other, a step of
+// results at a time: 16 steps (a tree of 32 on 2001 tokens) 24.8 us instead of
+// 16.8, 4 steps (two tokens of eight results) 11.5 instead of 14.4.
+constexpr int JOIN_HERE_WGS = 256, JOIN_HERE_STEPS = 6;
 
 template <int DT, int D>
-hipError_t run(const AttendArgs &a, int n_groups, int n_tokens, hipStream_t st) {
-    return static_cast<long>(n_groups) * a.kv_heads <= JOIN_HERE_WGS ? run<DT, D, true>(a, n_groups, n_tokens, st)
-                                                                     : run<DT, D, false>(a, n_groups, n_tokens, st);
+hipError_t run(const AttendArgs &a, int n_groups, int n_tokens, int join_steps, hipStream_t st) {
+    const bool here = static_cast<long>(n_groups) * a.kv_heads <= JOIN_HERE_WGS && join_steps <= JOIN_HERE_STEPS;
+    return here ? run<DT, D, true>(a, n_groups, n_tokens, st) : run<DT, D, false>(a, n_groups, n_tokens, st);
 }
 
 }  // namespace
 
-hipError_t launch_attend(const AttendArgs &args, int dtype, int dim, int n_groups, int n_tokens, hipStream_t st) {
+hipError_t launch_attend(const AttendArgs &args, int dtype, int dim, int n_groups, int n_tokens, int join_steps,
+                         hipStream_t st) {
     AttendArgs a = args;
     if (dtype == DT_F16)
-        return dim == 128 ? run<DT_F16, 128>(a, n_groups, n_tokens, st) : run<DT_F16, 64>(a, n_groups, n_tokens, st);
+        return dim == 128 ? run<DT_F16, 128>(a, n_groups, n_tokens, join_steps, st)
+                          : run<DT_F16, 64>(a, n_groups, n_tokens, join_steps, st);
     a.scale *= static_cast<float>(1u << KEXP_LESS);
-    return dim == 128 ? run<DT_BF16, 128>(a, n_groups, n_tokens, st) : run<DT_BF16, 64>(a, n_groups, n_tokens, st);
+    return dim == 128 ? run<DT_BF16, 128>(a, n_groups, n_tokens, join_steps, st)
+                      : run<DT_BF16, 64>(a, n_groups, n_tokens, join_steps, st);
 }
 
 }  // namespace lora

@@ -99,7 +99,7 @@ void AttendPlanner::clear() {
     pages_.clear();
     nodes_.clear();
     spans_.clear();
-    part_rows_ = n_split_ = 0;
+    part_rows_ = join_steps_ = n_split_ = 0;
 }
 
 int AttendPlanner::check(const AttendBatch &b, const AttendGeometry &geo) const {
@@ -319,7 +319,14 @@ int AttendPlanner::plan(const AttendBatch &b, const AttendGeometry &geo) {
                 t.stride[s.own] = s.n_tok;
             }
         }
-        if (!alone) part_rows_ += splits * s.n_tok;
+        if (alone) continue;
+        part_rows_ += splits * s.n_tok;
+        int steps = 0;
+        for (int i = 0; i < s.n_tok; ++i) {
+            const AttendToken &t = tokens_[static_cast<size_t>(s.tok0 + i)];
+            steps += ceil_div(t.n[0] + t.n[1], ATTEND_JOIN_STEP);
+        }
+        join_steps_ = std::max(join_steps_, steps);
     }
     for (AttendToken &t : tokens_) {
         if (t.pad) t.n[0] = t.n[1] = 0;

@@ -74,6 +74,7 @@ constexpr int ATTEND_MAX_KEYS = 1 << 30;  // keys of one sequence or prefix (til
 constexpr int ATTEND_ROWS = 32;       // query rows (tokens x heads of a key head) of an item
 constexpr int ATTEND_SLOTS = 2048;    // waves that run at once: two workgroups on each of 256 CUs
 constexpr int ATTEND_NODE_PAD = 64;   // words before and after the nodes: the tile that holds one may begin, and end, so far away
+constexpr int ATTEND_JOIN_STEP = 4;   // results of a token that are read together
 constexpr int ATTEND_EXTRA = 1024;    // workgroups that splitting may add, over all key/value heads
 
 // A token of a tree as the kernels read it, and whether i is j or above it.
@@ -128,6 +129,9 @@ public:
     const std::vector<int32_t> &pages() const { return pages_; }
     const std::vector<uint32_t> &nodes() const { return nodes_; }  // of the sorted tokens; empty: no trees
     int part_rows() const { return part_rows_; }
+    // What the last item of a block has to join at most, in steps of up to four
+    // results of one token.
+    int join_steps() const { return join_steps_; }
     int n_split() const { return n_split_; }
 
 private:
@@ -156,7 +160,7 @@ private:
     std::vector<char> tree_;            // of each sequence: not a mere chain
     std::vector<Span> spans_;
     std::vector<int32_t> seq_tok_, grp_tok_, seq_page_, grp_page_, q_first_;
-    int part_rows_ = 0, n_split_ = 0, page_size_ = 0, n_pages_ = 0;
+    int part_rows_ = 0, join_steps_ = 0, n_split_ = 0, page_size_ = 0, n_pages_ = 0;
 };
 
 }  // namespace lora

@@ -407,6 +407,7 @@ int lora_attend(lora_kv kv, lora_attend_plan plan, const void *q, int64_t q_stri
         kv->page_size != plan->page_size || kv->c.n_pages != plan->n_pages)
         return LORA_EMISMATCH;
     int n_tokens = static_cast<int>(plan->planner.tokens().size()), n_groups = plan->planner.groups();
+    int join_steps = plan->planner.join_steps();
     DeviceGuard g(plan->device);
     HIP_TRY(g.error());
     if (n_tokens == 0) {
@@ -415,7 +416,7 @@ int lora_attend(lora_kv kv, lora_attend_plan plan, const void *q, int64_t q_stri
         hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
         HIP_TRY(hipStreamIsCapturing(static_cast<hipStream_t>(stream), &cap));
         if (cap == hipStreamCaptureStatusNone) return LORA_OK;
-        n_tokens = plan->max_tokens;
+        n_tokens = join_steps = plan->max_tokens;
         n_groups = (lora::ATTEND_SLOTS / lora::ATTEND_WAVES + plan->n_kv_heads - 1) / plan->n_kv_heads;
     }
     const int64_t row = static_cast<int64_t>(plan->n_heads) * plan->head_dim;
@@ -441,7 +442,7 @@ int lora_attend(lora_kv kv, lora_attend_plan plan, const void *q, int64_t q_stri
     a.page_shift = kv->c.page_shift;
     a.n_pages = kv->c.n_pages;
     a.scale = scale * 1.44269504088896340736f;
-    HIP_TRY(lora::launch_attend(a, kv->c.dtype, plan->head_dim, n_groups, n_tokens,
+    HIP_TRY(lora::launch_attend(a, kv->c.dtype, plan->head_dim, n_groups, n_tokens, join_steps,
                                 static_cast<hipStream_t>(stream)));
     return LORA_OK;
 }

@@ -87,7 +87,9 @@ struct AttendArgs {
     float scale;           // softmax scale times log2(e)
 };
 
-hipError_t launch_attend(const AttendArgs &a, int dtype, int dim, int n_groups, int n_tokens, hipStream_t st);
+// join_steps: AttendPlanner's.
+hipError_t launch_attend(const AttendArgs &a, int dtype, int dim, int n_groups, int n_tokens, int join_steps,
+                         hipStream_t st);
 
 struct VerifyArgs {
     const void *p, *q;

@@ -659,7 +659,8 @@ int lora_verify(lora_verifier v, const void *p_target, const void *p_draft, lora
  *              never come to
  *   row0       device int32 [n_seqs + 1], strictly ascending from 0 to n_rows
  *   u          device float [n_rows], of [0, 1)
- *   accepted   device int32 [n_seqs]: how many drafted tokens were kept, k
+ *   accepted   device int32 [n_seqs]: how many drafted tokens were kept, k.  It
+ *              and the next two share no memory with the inputs or each other
  *   tokens     device int32 [n_rows]: at row0[s] the k kept tokens, then the
  *              last one drawn, then -1
  *   path       device int32 [n_rows]: at row0[s] the k + 1 nodes that these

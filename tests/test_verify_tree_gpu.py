@@ -149,6 +149,20 @@ def test_bounds_that_overlap():
     lora.lora_verifier_destroy(v)
 
 
+@pytest.mark.parametrize("bad", [[0, 1000, 2, 1002, 1010], [0, 700, 1, 2, 1010], [0, 1001, 3, 1003, 1010]])
+def test_large_trees_that_overlap(bad):
+    """The same of trees past 512 nodes, whose lists lie in memory that
+    sequences with the same rows share: the walks end inside their trees."""
+    p, draft, parent, row0, u = batch(["near"] * 4, [400, 400, 200, 10], 16, "f32", 3)
+    v = lora.lora_verifier_create(4)
+    tokens, path, accepted = call(p, draft, parent, bad, u, verifier=v)
+    fits = [b <= bad[b] < bad[b + 1] <= 1010 - (3 - b) for b in range(4)]
+    assert all((a == -1) if not f else (-1 <= a < bad[b + 1] - bad[b]) for b, (a, f) in enumerate(zip(accepted, fits)))
+    assert all(-1 <= t < 16 or t == -7 for t in tokens) and all(-1 <= n < 1010 or n == -7 for n in path)
+    assert call(p, draft, parent, row0, u, verifier=v) == same(p, draft, parent, row0, u)  # the next call is whole
+    lora.lora_verifier_destroy(v)
+
+
 @pytest.mark.parametrize("unit", [8, 512, 32768])
 def test_a_place_without_weight_is_not_drawn(unit):
     """As for lora_verify: weights whose order of adding decides about 1/2."""

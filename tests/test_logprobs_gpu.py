@@ -134,6 +134,41 @@ def test_equal_logits(dtype, vocab):
             check(z, t, 1.0, top, got)
 
 
+@pytest.mark.parametrize("n,vocab,threads", [(2, 131072, 1024), (600, 20000, 256)])
+def test_many_above_the_first_bound(n, vocab, threads):
+    """Where only 31 of the 64 groups of lanes hold anything high, and ascending,
+    the 32nd alternative's first bound leaves nearly half of the row, and every
+    next one the rest but for a few hundred."""
+    i = torch.arange(vocab, device="cuda")
+    group = (i // 512 % (threads // 64) * 64 + i // 8 % 64) // (threads // 64)
+    z = torch.where(group < 31, i.float() / vocab, -10.0 - i.float() / vocab).expand(n, vocab).contiguous()
+    t = tokens_for(n, vocab, n)
+    with Scorer(n) as s:
+        got = buffers(n, 32)
+        lora.lora_logprobs(s, z, t.cuda(), 1.0, *got)
+        check(z[:3], t[:3], 1.0, 32, [x[:3] for x in got])
+        assert all((x[3:] == x[3:4]).all() for x in got[1:])  # entropy and alternatives: rows are alike
+
+
+def test_two_at_once():
+    """Two scorers on two streams, several calls each way in flight."""
+    rows = [logits(3, 131072, "f32", 5), logits(4, 140001, "bf16", 6)]
+    t = [tokens_for(len(z), z.shape[1], 9) for z in rows]
+    on = [x.cuda() for x in t]
+    got = [[buffers(len(z), 7) for _ in range(8)] for z in rows]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in rows]
+    with Scorer(4) as a, Scorer(4) as b:
+        for i in range(8):
+            for k, s in enumerate((a, b)):
+                lora.lora_logprobs(s, rows[k], on[k], 1.0, *got[k][i], stream=streams[k])
+        torch.cuda.synchronize()
+    for k, z in enumerate(rows):
+        check(z, t[k], 1.0, 7, got[k][0])
+        for other in got[k][1:]:
+            assert all(torch.equal(x.nan_to_num(3.0), y.nan_to_num(3.0)) for x, y in zip(got[k][0], other))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("vocab", [64, 5000, 66000])
 def test_masks(dtype, vocab):

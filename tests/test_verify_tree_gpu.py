@@ -243,3 +243,22 @@ def test_captured_and_replayed(V, sizes):
         torch.cuda.synchronize()
         assert tuple(x.tolist() for x in out) == same(*new)
     lora.lora_verifier_destroy(v)
+
+
+def test_two_at_once():
+    """Two verifiers on two streams, several calls each way in flight."""
+    some = [batch(["near"] * 3, [9, 1, 30], 70000, "bf16", 11), batch(["binary"] * 2, [16, 5], 140001, "f32", 12)]
+    streams = [torch.cuda.Stream() for _ in some]
+    vs = [lora.lora_verifier_create(3) for _ in some]
+    on = [(torch.tensor(d, **I), torch.tensor(up, **I), torch.tensor(r, **I), torch.tensor(u, dtype=torch.float32, device="cuda"))
+          for _, d, up, r, u in some]
+    out = [[tuple(torch.full((n,), -7, **I) for n in (r[-1], r[-1], len(r) - 1)) for _ in range(8)] for _, _, _, r, _ in some]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for k, (p, _, _, r, _) in enumerate(some):
+            lora.lora_verify_tree(vs[k], p, *on[k], len(r) - 1, r[-1], *out[k][i], stream=streams[k])
+    torch.cuda.synchronize()
+    for k, (p, d, up, r, u) in enumerate(some):
+        want = same(p, d, up, r, u)
+        assert all(tuple(x.tolist() for x in o) == want for o in out[k])
+        lora.lora_verifier_destroy(vs[k])

@@ -700,7 +700,7 @@ int lora_scorer_destroy(lora_scorer s);
  *             looked at where top is 0
  * Logits of -inf have probability 0.  A row that holds NaN or +inf, or nothing
  * above -inf, is no distribution: its results are NaN, its top_ids -1.
- * Sums are held in fp32 against each wave's largest logit and joined in a fixed
+ * Sums are held in fp32 against each lane's largest logit and joined in a fixed
  * order.  Errors (nothing enqueued): LORA_EINVAL, LORA_ETOKENS (n_rows),
  * LORA_EHIP.
  * Calls on one scorer on different streams are ordered by the caller. */

@@ -587,13 +587,21 @@ def _batch(q_len, kv_len, group, pages, page0, prefix_len=None, prefix_pages=Non
                              *lists(prefix_pages, prefix_page0, n_groups, "prefix_pages", "prefix_page0"))
 
 
+def _plan_set(plan, tokens, entry, *args):
+    """The library's call for a batch of `tokens`.  The plan's tokens, which
+    lora_attend's outputs are checked by, change when the library's plan does:
+    to none where it refuses the batch, and not at all where the binding does."""
+    known = _attend_plans[plan]
+    rc = entry(plan, *args)
+    known[2] = tokens if rc == LORA_OK else 0
+    _check(rc, entry.__name__)
+
+
 def lora_attend_plan_set(plan, kv, q_len, kv_len, group, pages, page0, prefix_len=None, prefix_pages=None,
                          prefix_page0=None, stream=None):
     """The batch's lists as host int32 tensors (lora_attend_batch in lora.h)."""
     b = _batch(q_len, kv_len, group, pages, page0, prefix_len, prefix_pages, prefix_page0)
-    _attend_plans[plan][2] = 0
-    _check(_lib.lora_attend_plan_set(plan, kv, ctypes.byref(b), _stream(stream)), "lora_attend_plan_set")
-    _attend_plans[plan][2] = int(q_len.sum())
+    _plan_set(plan, int(q_len.sum()), _lib.lora_attend_plan_set, kv, ctypes.byref(b), _stream(stream))
 
 
 def lora_attend_plan_set_tree(plan, kv, parent, q_len, kv_len, group, pages, page0, prefix_len=None,
@@ -604,10 +612,8 @@ def lora_attend_plan_set_tree(plan, kv, parent, q_len, kv_len, group, pages, pag
     n = int(q_len.sum())
     if parent is None:
         raise ValueError("parent: expected %d elements, got none" % n)
-    _attend_plans[plan][2] = 0
-    _check(_lib.lora_attend_plan_set_tree(plan, kv, ctypes.byref(b), _host(parent, n, "parent"), _stream(stream)),
-           "lora_attend_plan_set_tree")
-    _attend_plans[plan][2] = n
+    _plan_set(plan, n, _lib.lora_attend_plan_set_tree, kv, ctypes.byref(b), _host(parent, n, "parent"),
+              _stream(stream))
 
 
 def lora_attend(kv, plan, q, scale, out, lse=None, stream=None):

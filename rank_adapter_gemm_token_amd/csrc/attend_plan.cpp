@@ -138,6 +138,7 @@ int AttendPlanner::check(const AttendBatch &b, const AttendGeometry &geo) const 
         if (!row(b.prefix_pages, b.prefix_page0, i, b.prefix_len[i])) return LORA_EINVAL;
     if (tokens > max_tokens_) return LORA_ETOKENS;
     if (pages > max_pages_) return LORA_EINVAL;
+    if (b.tree && tokens > 0 && b.parent == nullptr) return LORA_EINVAL;
     if (b.parent != nullptr) {
         const int32_t *parent = b.parent;
         for (int s = 0; s < b.n_seqs; parent += b.q_len[s], ++s)

@@ -93,8 +93,9 @@ struct AttendBatch {
     const int32_t *pages, *page0;
     const int32_t *prefix_len, *prefix_pages, *prefix_page0;
     // Of each new token the new token of its sequence that it follows, or -1;
-    // null: each follows the one before.
+    // null: each follows the one before, unless the list has to be there.
     const int32_t *parent;
+    bool tree = false;  // it has to be, where there are new tokens
 };
 
 struct AttendGeometry {

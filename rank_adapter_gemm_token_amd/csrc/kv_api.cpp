@@ -111,19 +111,21 @@ bool rows_ok(const lora_kv_s *kv, const void *k, int64_t k_stride, const void *v
            aligned(v, 16) && aligned(slots, 4) && k_stride % 8 == 0 && v_stride % 8 == 0;
 }
 
-// Checks and cuts a batch on the host.
-int plan_batch(lora_attend_plan plan, lora_kv kv, const lora_attend_batch *batch, const int32_t *parent) {
+// Checks and cuts a batch on the host.  tree: `parent` has to be there, if there
+// are new tokens.
+int plan_batch(lora_attend_plan plan, lora_kv kv, const lora_attend_batch *batch, const int32_t *parent, bool tree) {
     if (kv == nullptr || batch == nullptr) return LORA_EINVAL;
     if (kv->device != plan->device || kv->c.heads != plan->n_kv_heads || kv->c.dim != plan->head_dim)
         return LORA_EMISMATCH;
     const lora::AttendBatch b{batch->n_seqs, batch->n_groups, batch->q_len, batch->kv_len, batch->group,
                               batch->pages, batch->page0, batch->prefix_len, batch->prefix_pages,
-                              batch->prefix_page0, parent};
+                              batch->prefix_page0, parent, tree};
     return plan->planner.plan(b, lora::AttendGeometry{plan->n_heads, plan->n_kv_heads, kv->page_size, kv->c.n_pages});
 }
 
 // The plan of a batch, to the device.
-int set_plan(lora_attend_plan plan, lora_kv kv, const lora_attend_batch *batch, const int32_t *parent, void *stream) {
+int set_plan(lora_attend_plan plan, lora_kv kv, const lora_attend_batch *batch, const int32_t *parent, bool tree,
+             void *stream) {
     if (plan == nullptr) return LORA_EINVAL;
     std::lock_guard<std::mutex> lk(plan->mu);
     plan->set = false;  // until this batch is on its way, whatever refuses it
@@ -134,7 +136,7 @@ int set_plan(lora_attend_plan plan, lora_kv kv, const lora_attend_batch *batch, 
     hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
     HIP_TRY(hipStreamIsCapturing(st, &cap));
     if (cap != hipStreamCaptureStatusNone) return LORA_EINVAL;
-    const int rc = plan_batch(plan, kv, batch, parent);
+    const int rc = plan_batch(plan, kv, batch, parent, tree);
     // A refused batch leaves the device a plan for no cache, so that graphs do
     // not attend to the one before.
     if (rc != LORA_OK && plan->sent_tokens < 0) return rc;
@@ -386,16 +388,12 @@ int lora_attend_plan_destroy(lora_attend_plan plan) {
 }
 
 int lora_attend_plan_set(lora_attend_plan plan, lora_kv kv, const lora_attend_batch *batch, void *stream) {
-    return set_plan(plan, kv, batch, nullptr, stream);
+    return set_plan(plan, kv, batch, nullptr, false, stream);
 }
 
 int lora_attend_plan_set_tree(lora_attend_plan plan, lora_kv kv, const lora_attend_batch *batch,
                               const int32_t *parent, void *stream) {
-    // Without new tokens there is no list to give.
-    bool missing = false;
-    if (parent == nullptr && batch != nullptr && batch->q_len != nullptr)
-        for (int s = 0; s < batch->n_seqs; ++s) missing = missing || batch->q_len[s] != 0;
-    return set_plan(plan, kv, missing ? nullptr : batch, parent, stream);
+    return set_plan(plan, kv, batch, parent, true, stream);
 }
 
 int lora_attend(lora_kv kv, lora_attend_plan plan, const void *q, int64_t q_stride, float scale, void *out,

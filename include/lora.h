@@ -701,7 +701,7 @@ int lora_scorer_destroy(lora_scorer s);
  * Logits of -inf have probability 0.  A row that holds NaN or +inf, or nothing
  * above -inf, is no distribution: its results are NaN, its top_ids -1.
  * Sums are held in fp32 against each lane's largest logit and joined in a fixed
- * order.  Errors (nothing enqueued): LORA_EINVAL, LORA_ETOKENS (n_rows),
+ * order; no log probability comes out above 0 and no entropy below.  Errors (nothing enqueued): LORA_EINVAL, LORA_ETOKENS (n_rows),
  * LORA_EHIP.
  * Calls on one scorer on different streams are ordered by the caller. */
 int lora_logprobs(lora_scorer s, const void *logits, int64_t stride, lora_dtype dtype, int vocab,

@@ -320,9 +320,13 @@ __device__ __forceinline__ void put(const LogprobsArgs &a, int row, const Stats 
     constexpr double LN2 = 0.69314718055994530942;
     const float nan = __uint_as_float(Elem<DT_F32>::qnan);
     // log2 l: the exponent is exact, and the logarithm of what is left below 1.
+    // The largest logit's own term makes l 1 at least, but the term's two
+    // exponentials (Row::stats) and the logarithm are rounded: without the bounds
+    // here and below a sure row's log probability came out as +6e-8 and its
+    // entropy as -6e-8.
     int exponent;
     const float left = frexpf(all.l, &exponent);
-    const double log_l = static_cast<double>(exponent) + static_cast<double>(__log2f(left));
+    const double log_l = fmax(static_cast<double>(exponent) + static_cast<double>(__log2f(left)), 0.0);
     // Lane `top` has the given token.
     const uint64_t key = lane < a.top ? best[lane] : 0;
     const float v = lane < a.top ? of_order(static_cast<uint32_t>(key >> 32)) : zt;
@@ -335,7 +339,7 @@ __device__ __forceinline__ void put(const LogprobsArgs &a, int row, const Stats 
     } else if (lane == a.top) {
         if (a.logprob != nullptr) a.logprob[row] = known ? log_p : nan;
         if (a.entropy != nullptr)
-            a.entropy[row] = none ? nan : static_cast<float>(LN2 * (log_l - static_cast<double>(all.s) / static_cast<double>(all.l)));
+            a.entropy[row] = none ? nan : static_cast<float>(LN2 * fmax(log_l - static_cast<double>(all.s) / static_cast<double>(all.l), 0.0));
     }
 }
 

@@ -62,7 +62,9 @@ __device__ __forceinline__ float moved(float v, Op op) {
     return op(v, __uint_as_float(__builtin_amdgcn_update_dpp(__float_as_uint(v), __float_as_uint(v), CTRL, 0xf, 0xf, false)));
 }
 
-// Over the 4, 16 and 64 lanes about each.
+// Over the 4, 16 and 64 lanes about each.  In every step two lanes that are
+// joined give the same result to both, so that a sum is rounded alike in all
+// lanes: a token has one log probability, whichever lane writes it.
 template <typename Op>
 __device__ __forceinline__ float over4(float v, Op op) {
     v = moved<0xB1>(v, op);   // quad_perm: lanes 1 0 3 2
@@ -71,8 +73,8 @@ __device__ __forceinline__ float over4(float v, Op op) {
 template <typename Op>
 __device__ __forceinline__ float over16(float v, Op op) {
     v = over4(v, op);
-    v = moved<0x124>(v, op);  // row_ror:4
-    return moved<0x128>(v, op);
+    v = moved<0x128>(v, op);  // row_ror:8
+    return moved<0x124>(v, op);  // row_ror:4, of lanes alike 8 apart
 }
 template <typename Op>
 __device__ __forceinline__ float over64(float v, Op op) {
@@ -106,8 +108,10 @@ __device__ __forceinline__ Stats join(const Stats &a, const Stats &b, float c) {
     return Stats{m, a.l * ea + b.l * eb, a.s * ea + product(a.l * ea, ya) + b.s * eb + product(b.l * eb, yb)};
 }
 
-// The same of all lanes' (a lane without any: -inf, 0, 0).
+// The same of all lanes' (a lane without any: -inf, 0, 0), alike in all of them:
+// the products are rounded before they are added, not fused into one lane's sum.
 __device__ __forceinline__ Stats join_lanes(const Stats &a, float c) {
+#pragma clang fp contract(off)
     const float m = over64(a.m, Max()), ref = m == -INFINITY ? 0.0f : m;
     const float y = (a.m - ref) * c, e = exp2_fast(y), l = a.l * e;
     return Stats{m, over64(l, Sum()), over64(a.s * e + product(l, y), Sum())};

@@ -684,8 +684,9 @@ int lora_scorer_create(int max_rows, lora_scorer *out);
 /* Waits for the device, then frees it.  s == NULL is a no-op. */
 int lora_scorer_destroy(lora_scorer s);
 
-/* Log probabilities under softmax(scale * logits), row by row, each logit read
- * once.
+/* Log probabilities under softmax(scale * logits), row by row.  Each logit is
+ * read once, and a few neighbourhoods once more where alternatives are asked
+ * for; a row of many equal logits is then looked through several times.
  *   logits    device, rows of `vocab` in dtype (any lora_dtype), `stride`
  *             elements apart (at least vocab); vocab 1 .. LORA_VERIFY_MAX_VOCAB
  *   tokens    device int32 [n_rows]: the token to score, or one outside the

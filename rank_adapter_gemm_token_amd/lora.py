@@ -522,9 +522,13 @@ def lora_rope_destroy(rope):
 
 def lora_kv_append(kv, rope, k, v, slots, positions, n_tokens, q=None, q_out=None, stream=None):
     """k, v, slots as for lora_kv_write; positions: device int32 of n_axes *
-    n_tokens elements; q, q_out: [n_tokens, n_heads, head_dim], strided over
-    tokens, or None; q_out may be q."""
+    n_tokens elements, [n_axes, n_tokens] or flat; q, q_out: [n_tokens, n_heads,
+    head_dim], strided over tokens, or None; q_out may be q."""
     heads, dim, dtype = _kvs[kv]
+    axes = _ropes[rope]
+    # The axes lie n_tokens apart.  Rows of a longer buffer would be read at the wrong places.
+    if axes > 1 and n_tokens > 0 and positions.dim() > 1 and positions.shape[-1] != n_tokens:
+        raise ValueError("positions: expected [%d, %d], got %s" % (axes, n_tokens, tuple(positions.shape)))
     kp, ks = _rows(k, n_tokens, heads, dim, dtype, "k")
     vp, vs = _rows(v, n_tokens, heads, dim, dtype, "v")
     qp = op = None
@@ -536,7 +540,7 @@ def lora_kv_append(kv, rope, k, v, slots, positions, n_tokens, q=None, q_out=Non
             raise ValueError("q_out: expected a tensor for the turned queries, got none")
         op, os_ = _rows(q_out, n_tokens, n_heads, dim, dtype, "q_out")
     _check(_lib.lora_kv_append(kv, rope, kp, ks, vp, vs, _flat(slots, n_tokens, torch.int32, "slots"),
-                               _flat(positions, _ropes[rope] * n_tokens, torch.int32, "positions"), n_tokens, qp, qs,
+                               _flat(positions, axes * n_tokens, torch.int32, "positions"), n_tokens, qp, qs,
                                n_heads, op, os_, _stream(stream)), "lora_kv_append")
 
 

@@ -217,6 +217,14 @@ __device__ __forceinline__ void join_parts(const AttendArgs &a, const AttendToke
     put_out<DT, D>(a, tk.token, head, d, sum, M, L);
 }
 
+// The lane's number, counted where it is asked for: a value that the compiler
+// does not keep, and spill, in between.
+__device__ __forceinline__ int lane_anew() {
+    int lane;
+    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=&v"(lane));
+    return lane;
+}
+
 // One wave's item for one key/value head.  QB blocks of 16 query rows; row =
 // token of the item x query head of the key head.
 template <int DT, int D, int QB, bool HERE>
@@ -227,11 +235,10 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
     constexpr int NC = D / 64;   // 64-element parts of a key's row: 16 bytes a lane each
     constexpr int NH = D / 16;   // 16-element rows of V^T
     constexpr int ROWS = 16 * QB;
-    int lane = threadIdx.x & 63;
-    // Made anew for each item: the compiler would keep, and spill, addresses
-    // made of it over all of them (8 registers; one sequence 10.2 us for 9.65).
-    asm volatile("" : "+v"(lane));
-    const int r = lane & 15, g = lane >> 4;
+    // Made anew for each item, in the branch for masks and after the loop: the
+    // compiler would keep, and spill, addresses made of it over all of them (3 to
+    // 8 registers; one sequence of 2001 tokens 9.9 us instead of 9.4).
+    int lane = lane_anew(), r = lane & 15, g = lane >> 4;
     const bool joined = (it.flags & ATTEND_JOINED) != 0;
     const int step = joined ? ATTEND_WAVES : 1;
 
@@ -362,10 +369,11 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
     for (int b = 0; b < QB; ++b)
 #pragma unroll
         for (int i = 0; i < 2 * NC; ++i) qf[(b * 2 * NC + i) * 64] = q0[b][i];
-    int *row_token = reinterpret_cast<int *>(qf - lane + QB * 2 * NC * 64) + r;
+    // The rows' tokens, behind the queries.
+    auto token_in_lds = [&] { return reinterpret_cast<int *>(lds + wave * wave_floats(D) + QB * 2 * NC * 256); };
     if (g == 0)
 #pragma unroll
-        for (int b = 0; b < QB; ++b) row_token[b * 16] = tok[b];
+        for (int b = 0; b < QB; ++b) token_in_lds()[b * 16 + r] = tok[b];
 
     auto tile = [&](auto more) __attribute__((always_inline)) {
         asm volatile("" ::: "memory");  // the queries are read again, not kept
@@ -428,9 +436,8 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
         }
         if (uniform(key0 + ATTEND_TILE > all)) {
             asm volatile("");  // a branch: as selects it would cost every tile 100 instructions
-            int row = r;
-            asm volatile("" : "+v"(row));  // what is made of it is not kept over the loop
-            uint32_t hidden[QB];           // bit i: key 16 g + i of the tile
+            const int lane = lane_anew(), r = lane & 15, g = lane >> 4;
+            uint32_t hidden[QB];  // bit i: key 16 g + i of the tile
             if (in_tree) {
                 // Lane n looks at key key0 + n, whose node is at that place of
                 // the shifted list (which reaches a tile past the nodes on both
@@ -446,12 +453,12 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
                     const uint32_t half = g < 2 ? static_cast<uint32_t>(all) : static_cast<uint32_t>(all >> 32);
 #pragma unroll
                     for (int b = 0; b < QB; ++b)
-                        if (token_of_row(a, b * 16 + row) == n) hidden[b] = half >> (16 * (g & 1));
+                        if (token_of_row(a, b * 16 + r) == n) hidden[b] = half >> (16 * (g & 1));
                 }
             } else {
 #pragma unroll
                 for (int b = 0; b < QB; ++b) {
-                    const int i = token_of_row(a, b * 16 + row);
+                    const int i = token_of_row(a, b * 16 + r);
                     const int seen = it.limit0 + ((it.flags & ATTEND_STEP) && i < it.n_tok ? i : 0);
                     const int n = (seen < it.end ? seen : it.end) - (key0 + 16 * g);  // of the lane's keys
                     hidden[b] = n >= 16 ? 0u : n <= 0 ? 0xFFFFu : 0xFFFFu << n;
@@ -539,6 +546,8 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
     for (; t + step < t_end; t += step) tile(std::true_type());
     if (t < t_end) tile(std::false_type());
 
+    lane = lane_anew(), r = lane & 15, g = lane >> 4;
+    const int thread = wave * 64 + lane;
     float m[QB];
 #pragma unroll
     for (int b = 0; b < QB; ++b) {
@@ -555,7 +564,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
             if (i < it.n_tok)
 #pragma unroll
                 for (int h = 0; h < NH; ++h)
-                    emit<DT, D, HERE>(a, it, row_token[b * 16], i, kvh * a.gq + row - i * a.gq, h * 16 + g * 4, o[h][b], m[b], l[b]);
+                    emit<DT, D, HERE>(a, it, token_in_lds()[b * 16 + r], i, kvh * a.gq + row - i * a.gq, h * 16 + g * 4, o[h][b], m[b], l[b]);
         }
         if (!HERE || it.part0 < 0) return;
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -581,7 +590,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
     }
     __syncthreads();
     const int n_rows = it.n_tok * a.gq;
-    for (int at = threadIdx.x; at < n_rows * PER; at += 256) {
+    for (int at = thread; at < n_rows * PER; at += 256) {
         const int row = at / PER, d = at % PER * 4;
         float mw[ATTEND_WAVES], M = -INFINITY, L = 0.0f;
 #pragma unroll
@@ -612,7 +621,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs &a, const AttendIte
         unsigned long long todo = *last;
         for (; todo != 0; todo &= todo - 1) {
             const AttendToken tk = toks[__builtin_ctzll(todo)];
-            for (int at = threadIdx.x; at < a.gq * PER; at += 256)
+            for (int at = thread; at < a.gq * PER; at += 256)
                 join_parts<DT, D, HERE>(a, tk, kvh * a.gq + at / PER, at % PER * 4);
         }
     }
@@ -709,7 +718,9 @@ hipError_t run(const AttendArgs &a, int n_groups, int n_tokens, hipStream_t st) 
 // instead of 55; 64 decoding ones, 1200: 49 instead of 43).  So: up to one a
 // CU.  And the last of a block joins one token after the other, a step of
 // results at a time: 16 steps (a tree of 32 on 2001 tokens) 24.8 us instead of
-// 16.8, 4 steps (two tokens of eight results) 11.5 instead of 14.4.
+// 16.8, 4 steps (two tokens of eight results) 11.5 instead of 14.4.  At 8 steps
+// it goes by the sequences: one with four tokens 13.5 instead of 14.1, two 14.1
+// instead of 13.4, four 14.6 instead of 13.4.
 constexpr int JOIN_HERE_WGS = 256, JOIN_HERE_STEPS = 6;
 
 template <int DT, int D>

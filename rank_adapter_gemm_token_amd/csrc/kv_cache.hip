@@ -90,14 +90,14 @@ struct Words {
     }
 };
 
-// Elements of a row, N of them as bytes in N / 4 words.
-template <int N>
-__device__ __forceinline__ void quantise(const float (&x)[N], int byte, uint32_t (&w)[N / 4]) {
+// Elements x(0) .. x(N - 1) of a row as bytes in N / 4 words.
+template <int N, typename X>
+__device__ __forceinline__ void quantise(X x, int byte, uint32_t (&w)[N / 4]) {
     const float inv = __uint_as_float(static_cast<uint32_t>(2 * KV_EXP_BIAS - byte) << 23);
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
-        int v = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * i] * inv, x[4 * i + 1] * inv, 0, false);
-        v = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * i + 2] * inv, x[4 * i + 3] * inv, v, true);
+        int v = __builtin_amdgcn_cvt_pk_fp8_f32(x(4 * i) * inv, x(4 * i + 1) * inv, 0, false);
+        v = __builtin_amdgcn_cvt_pk_fp8_f32(x(4 * i + 2) * inv, x(4 * i + 3) * inv, v, true);
         w[i] = static_cast<uint32_t>(v);
     }
 }
@@ -310,9 +310,9 @@ __device__ __forceinline__ void write_tile(const KvCache &c, const TurnArgs &tur
     auto put = [&](const Pair &x, int i, long R, uint32_t (&vw)[N / 4]) {
         float kx[N], vx[N], ka = 0.0f, va = 0.0f;
         bool fin = true;
-#pragma unroll
-        for (int e = 0; e < N; ++e) kx[e] = x.k.template at<DT>(e);
         if constexpr (STYLE != TURN_NONE) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) kx[e] = x.k.template at<DT>(e), vx[e] = x.v.template at<DT>(e);
             constexpr int M = pairs_of<N, STYLE>();
             const int n = turn.t.n;
             const Words<N> y = partners<N, STYLE>(x.k, n, l);
@@ -324,22 +324,32 @@ __device__ __forceinline__ void write_tile(const KvCache &c, const TurnArgs &tur
                     kx[e] = to_odd(turned<DT, double, N, STYLE>(x.k, y, e, a[(STYLE == TURN_PAIRS ? e / 2 : e) * (n / M)], l * N >= n));
             }
         }
+        // What was not turned is widened anew where it is used: in registers it
+        // would leave fewer workgroups a CU.
+        auto key = [&](int e) {
+            if constexpr (STYLE == TURN_NONE) return x.k.template at<DT>(e);
+            else return kx[e];
+        };
+        auto value = [&](int e) {
+            if constexpr (STYLE == TURN_NONE) return x.v.template at<DT>(e);
+            else return vx[e];
+        };
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-            vx[e] = x.v.template at<DT>(e);
             // A value that is not finite has the exponent bits all set (and
             // turns into one that is not); fmax drops NaN.
-            fin &= finite(kx[e]) && finite(vx[e]);
-            ka = fmaxf(ka, fabsf(kx[e]));
-            va = fmaxf(va, fabsf(vx[e]));
+            fin &= finite(key(e));
+            fin &= finite(value(e));
+            ka = fmaxf(ka, fabsf(key(e)));
+            va = fmaxf(va, fabsf(value(e)));
         }
         ka = max16(ka);
         va = max16(va);
         const bool poison = max16(fin ? 0.0f : 1.0f) != 0.0f;
         const int kb = poison ? KV_EXP_BIAS : exp_byte(ka), vb = poison ? KV_EXP_BIAS : exp_byte(va);
         uint32_t kw[N / 4];
-        quantise<N>(kx, kb, kw);
-        quantise<N>(vx, vb, vw);
+        quantise<N>(key, kb, kw);
+        quantise<N>(value, vb, vw);
         if (poison) {
 #pragma unroll
             for (int e = 0; e < N / 4; ++e) kw[e] = 0x7F7F7F7Fu, vw[e] = 0u;
@@ -438,7 +448,7 @@ __device__ __forceinline__ void write_tile(const KvCache &c, const TurnArgs &tur
 }
 
 template <int DT, int D>
-__global__ __launch_bounds__(256, 8) void k_kv_write(KvCache c, const uint16_t *k, int64_t k_stride, const uint16_t *v,
+__global__ __launch_bounds__(256) void k_kv_write(KvCache c, const uint16_t *k, int64_t k_stride, const uint16_t *v,
                                                   int64_t v_stride, const int32_t *slots, int n_tokens, int per,
                                                   int groups) {
     write_tile<DT, D, TURN_NONE>(c, TurnArgs{}, nullptr, k, k_stride, v, v_stride, slots, n_tokens, static_cast<int>(blockIdx.x),

@@ -34,3 +34,12 @@ def test_attention_keeps_no_registers_in_scratch():
     spilled = {k: (v["VGPRs Spill"], v["ScratchSize [bytes/lane]"]) for k, v in kernels.items()
                if v["VGPRs Spill"] != "0" or v["ScratchSize [bytes/lane]"] != "0"}
     assert not spilled
+
+
+def test_cache_writes_keep_what_they_need_in_registers():
+    """Eight waves a SIMD (64 registers), none of them saved and fetched back."""
+    kernels = {k: v for k, v in report("kv_cache.hip").items() if "k_kv_write" in k}
+    assert len(kernels) == 4
+    for k, v in kernels.items():
+        assert v["SGPRs Spill"] == v["VGPRs Spill"] == v["ScratchSize [bytes/lane]"] == "0", (k, v)
+        assert int(v["VGPRs"]) <= 64, (k, v)

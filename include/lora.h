@@ -649,7 +649,10 @@ int lora_verify(lora_verifier v, const void *p_target, const void *p_draft, lora
  * node's u: the first index at which the running sum, in fp64, passes u times
  * the whole.  The first child of the node that holds it is kept and the walk
  * goes on there; where none does, the walk ends.  So every token is distributed
- * as the target's, however the tree was drafted.
+ * as the target's, however the tree was drafted.  Either all rows are read at
+ * once or those of the walk one after the other, by the sizes alone and for
+ * walks of about six rows: longer ones of large batches take up to three times
+ * what all rows at once would.
  *   p_target   device [n_rows][vocab], probabilities in dtype (any lora_dtype);
  *              what is not above 0 counts as nothing
  *   draft      device int32 [n_rows]: the tokens of the nodes (of node 0: not

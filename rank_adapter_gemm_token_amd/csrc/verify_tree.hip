@@ -10,9 +10,11 @@
 // it, the lane and the entry are then found by running sums of the wave's
 // lanes.  Only the chunk that is drawn from is read again (a few KB).
 //
-// Bound by latency for one tree (32 nodes of 32000 entries, fp32: 9 us), by
-// memory where every row is drawn from at once (64 trees of up to 16, 131072
-// entries of 16 bits: 142 MB in 40 us, 3.6 TB/s).
+// Bound by latency for one tree (32 nodes of 32000 entries, fp32: 9 us).  Where
+// every row is drawn from at once (64 trees of up to 16, 131072 entries of 16
+// bits: 142 MB in 40 us, 3.6 TB/s, of 6.7 that reads alone reach), by reads and
+// draws that do not overlap: all workgroups run at once, read together, and then
+// go through the draws' barriers and second reads together.
 #include "dtype.hpp"
 #include "kv_internal.hpp"
 #include "row_eight.hpp"
@@ -335,6 +337,12 @@ hipError_t launch_verify_tree(const VerifyTreeArgs &args, int dtype, hipStream_t
     // 32000 fp32 entries: 31; 200: 81; 256 over 32000 in bf16: 63; 250 over 5000
     // in fp16: 25), the second by what the longest of the walks may come by,
     // some six rows (32; 41; 37; 33).  One tree of 32 over 32000: 9 or 13.
+    // The drafts' quality is not known here.  Six rows is what drawn trees come
+    // by; where more are kept, the walk is chosen all the same and takes longer:
+    // 128 chains of 32 over 131072 16-bit entries 73 us with 5 drafts kept, 251
+    // with 16, 464 with 31, all rows at once 207 (64 of 32 over 32000 in fp32:
+    // 31, 81, 150; 51 to 56).  Where none is kept it is the other way: 64 of 16
+    // over 131072 take 56 at once and would walk in 12.
     const double mb = 1e-6 * a.n_rows * static_cast<double>(a.vocab) * (dtype == DT_F32 ? 4 : 2);
     const double rows = 6.0 + mb / 5.5 + 0.0032 * a.n_rows;
     const double levels = a.n_rows < 6 * static_cast<double>(a.n_seqs) ? static_cast<double>(a.n_rows) / a.n_seqs : 6.0;

@@ -478,14 +478,15 @@ int lora_kv_read(lora_kv kv, const int32_t *slots, int n_tokens, void *k, void *
  *   n_positions  1 .. LORA_ROPE_MAX_POSITIONS: 0 .. n_positions - 1
  *   rot_dim      elements of a head that turn, its first ones: 16 .. 128, a
  *                multiple of 16; the others are left as they are
- *   freq         host [rot_dim / 2], finite
+ *   freq         host [rot_dim / 2], finite, the angles at n_positions - 1 too
  *   axis         host [rot_dim / 2], each 0 .. n_axes - 1; NULL: all 0
  *   n_axes       positions of a token, 1 .. LORA_ROPE_MAX_AXES (a picture's
  *                tokens have a time, a height and a width)
  *   pairs        nonzero: pair i is elements 2 i and 2 i + 1; 0: elements i and
  *                i + rot_dim / 2
  *   scale        above 0, at most 1024
- * Cosines and sines are held to 48 bits.  Bytes: 8 n_positions rot_dim.
+ * Angles are products in fp64, their cosines and sines held to 48 bits.  Bytes:
+ * 8 n_positions rot_dim.
  * Allocates once, here, and waits for the device.
  * Errors: LORA_EINVAL, LORA_ENOMEM, LORA_EHIP. */
 int lora_rope_create(int n_positions, int rot_dim, const double *freq, const int32_t *axis, int n_axes, int pairs,

@@ -243,7 +243,8 @@ int lora_rope_create(int n_positions, int rot_dim, const double *freq, const int
     const int n = rot_dim / 2;
     int32_t axes[64] = {};
     for (int i = 0; i < n; ++i) {
-        if (!std::isfinite(freq[i])) return LORA_EINVAL;
+        // Nor may the farthest angle overflow: it has no cosine.
+        if (!std::isfinite(freq[i]) || !std::isfinite(freq[i] * (n_positions - 1))) return LORA_EINVAL;
         if (axis != nullptr) axes[i] = axis[i];
         if (axes[i] < 0 || axes[i] >= n_axes) return LORA_EINVAL;
     }

@@ -20,7 +20,9 @@
 // in fp32 beside it, by workgroups of their own.  Bound by the chain slot ->
 // position -> angle -> store: 4096 tokens in eight runs, 32 and 8 heads of 128,
 // 31 us, of which the keys and values alone take 21 (12 where none is turned);
-// 64 tokens of 32 and 32 heads 8 us.
+// 64 tokens of 32 and 32 heads 8 us.  A workgroup's 38 KB of LDS, 32 of them
+// angles, leave four a CU, so that of those 4096 tokens the queries' workgroups
+// follow the keys' rather than run beside them.
 #include "dtype.hpp"
 #include "kv_internal.hpp"
 
@@ -507,8 +509,8 @@ __device__ __forceinline__ void turn_queries(const TurnArgs &a, Angle<float> *an
 }
 
 // The first write_wgs workgroups write keys and values, the others turn queries.
-// (In turn over the launch: 35 us instead of 31 for 4096 tokens of 32 and 8
-// heads.)
+// (In turn over the launch, four workgroups a CU there too: 35 us instead of 31
+// for 4096 tokens of 32 and 8 heads.)
 template <int DT, int D, int STYLE>
 __global__ __launch_bounds__(256) void k_kv_append(KvCache c, TurnArgs turn, const uint16_t *k, int64_t k_stride,
                                                    const uint16_t *v, int64_t v_stride, const int32_t *slots,
